@@ -41,6 +41,7 @@
  *     nibbles in -7..7; every row is split into 16-byte groups, and byte j of group g holds
  *     element 32g + j in bits 0-3 and element 32g + 16 + j in bits 4-7. The GEMM widens a
  *     nibble to the int8 16 n by masking alone;
+ *   - prepared INT8 weights: int8 [d_out, d_in] in -127..127, row-major, plain column order;
  *   - per-token scale (alpha_t, or sigma_t for Lloyd-Max), per-token mean, per-channel s_w
  *     and w_1: float32;
  *   - bias: bfloat16 [d_out] or NULL;
@@ -353,6 +354,121 @@ oq_status oq_linear_g64(const oq_plan* plan, const void* x_bf16, int64_t T, int6
                         const uint8_t* w_packed, const uint32_t* w_sz, const float* w_scale,
                         const float* w_rowsum, const void* bias_bf16, int64_t d_out,
                         void* y_bf16, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- INT8 weights -------------------------------------------------------------------- */
+
+/* Offline preparation of INT8 weights, for the projections a user keeps at 8 bits (the pages
+ * quantize weights to INT4 only; the steps are those of oq_prepare_weights with 127 for 7):
+ * every row of W goes through the plan's rotation without centering and is quantized per
+ * output channel, s_w[o] = max|W_R[o,:]| / 127, codes in -127..127; w_1[o] = sum_k W[o,k]
+ * (fp32, before rotation).
+ *   plan      its activation kind is not used here
+ *   w_bf16    [n_out, ldw] bf16, 16-byte aligned, ldw >= d, (ldw * 2) % 16 == 0
+ *   w_codes   int8 [n_out, d]; w_scale float [n_out]; w_rowsum float [n_out] */
+oq_status oq_prepare_weights_w8(const oq_plan* plan, const void* w_bf16, int64_t n_out,
+                                int64_t ldw, int8_t* w_codes, float* w_scale, float* w_rowsum,
+                                void* stream);
+
+/* W8A8 GEMM, the epilogue of oq_gemm_w4a8:
+ *   acc[t,o] = sum_k a[t,k] * w[o,k]                     (exact int32)
+ *   y[t,o]   = bf16( a_scale[t] * w_scale[o] * acc + mean[t] * w_rowsum[o] + bias[o] )
+ *   a        int8 [T, d_in], w_codes int8 [d_out, d_in], every int8 value allowed (d_in <= 32768
+ *            keeps the sums below 2^31)
+ *   other arguments, limits and out as for oq_gemm_w4a8. */
+oq_status oq_gemm_w8a8(const int8_t* a, const float* a_scale, const float* mean,
+                       const int8_t* w_codes, const float* w_scale, const float* w_rowsum,
+                       const void* bias_bf16, int64_t T, int64_t d_in, int64_t d_out,
+                       oq_out_kind out_kind, void* out, void* stream);
+
+/* oq_linear against INT8 weights: oq_rotate_quantize into `workspace`, then oq_gemm_w8a8, the
+ * same result as the two calls. The plan's activation kind must be OQ_ACT_INT8_ABSMAX (else
+ * OQ_ERR_INVALID_ARG); workspace (oq_linear_workspace_bytes) and other arguments as for
+ * oq_linear. */
+oq_status oq_linear_w8a8(const oq_plan* plan, const void* x_bf16, int64_t T, int64_t ldx,
+                         const int8_t* w_codes, const float* w_scale, const float* w_rowsum,
+                         const void* bias_bf16, int64_t d_out, void* y_bf16, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ---- attention input: head norms and position rotation ------------------------------- */
+
+typedef enum {
+  OQ_NORM_NONE = 0,          /* x as it is                                               */
+  OQ_NORM_RMS = 1,           /* x / sqrt(mean(x^2) + eps)                                */
+  OQ_NORM_LAYER = 2          /* (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)        */
+} oq_norm_kind;
+
+typedef enum {
+  OQ_ROPE_NONE = 0,          /* no rotation                                              */
+  OQ_ROPE_PAIRS = 1,         /* element 2i with element 2i + 1                           */
+  OQ_ROPE_HALVES = 2         /* element i with element i + rot_dim / 2                   */
+} oq_rope_kind;
+
+typedef enum {
+  OQ_W_INT4 = 0,             /* oq_prepare_weights                                       */
+  OQ_W_INT8 = 1              /* oq_prepare_weights_w8                                    */
+} oq_weight_kind;
+
+/* What happens to every query and key head of a token (the pages have no counterpart: the
+ * diffusion transformers whose projections they quantize norm and rotate queries and keys
+ * behind the projection). A head x of head_dim elements becomes n = norm(x) * weight + bias over
+ * its own elements, and the pair (u, v) at index i < rot_dim / 2 of a token at position p becomes
+ *     (u cos[p][i] - v sin[p][i],  u sin[p][i] + v cos[p][i]);
+ * elements from rot_dim on are left as the norm gives them. Everything is float32; the result is
+ * rounded to bf16 once.
+ *   head_dim     a multiple of 16 in [16, 256]; q_heads, k_heads >= 0, their sum in [1, 65536]
+ *   norm         oq_norm_kind; eps >= 0, finite
+ *   rope         oq_rope_kind; rot_dim a multiple of 16 in [16, head_dim] (ignored for NONE)
+ *   q_weight ... float [head_dim], one for all query (key) heads, or NULL (1, and 0 for a bias);
+ *                16-byte aligned
+ *   cos, sin     float [n_pos, rot_dim / 2], 16-byte aligned; n_pos >= 1 (ignored for NONE) */
+typedef struct {
+  int32_t head_dim, q_heads, k_heads;
+  int32_t norm, rope, rot_dim;
+  float eps;
+  const float *q_weight, *q_bias, *k_weight, *k_bias;
+  const float *cos, *sin;
+  int64_t n_pos;
+} oq_heads;
+
+/* Norm and rotation of the query and key heads of batch x seq tokens in one pass.
+ *   q, k          bf16, element e of head h of token s of batch b at
+ *                 b * strides[0] + s * strides[1] + h * strides[2] + e  (strides in elements,
+ *                 >= 0, multiples of 8; base 16-byte aligned), so that slices of a packed
+ *                 projection and head-major layouts are taken as they are. NULL with no such heads
+ *   q_out, k_out  bf16, strides of their own. An output may be its input (same pointer and
+ *                 strides); otherwise outputs overlap neither the inputs nor one another
+ *   positions     int32, position of token (b, s) at b * pos_batch_stride + s, or NULL: s.
+ *                 A negative position: the token is normed but not rotated (text tokens among
+ *                 image tokens, padding). A position >= n_pos is a mistake that the host cannot
+ *                 see: the token's rotated elements become NaN
+ * batch * seq <= 2^31 - 1; 0 launches nothing. */
+oq_status oq_qk_norm_rope(const oq_heads* heads, int64_t batch, int64_t seq, const void* q,
+                          const int64_t q_strides[3], const void* k, const int64_t k_strides[3],
+                          const int32_t* positions, int64_t pos_batch_stride, void* q_out,
+                          const int64_t q_out_strides[3], void* k_out,
+                          const int64_t k_out_strides[3], void* stream);
+
+/* Bytes of device workspace oq_linear_qkv needs (0 for invalid arguments). */
+size_t oq_linear_qkv_workspace_bytes(const oq_plan* plan, const oq_heads* heads,
+                                     oq_weight_kind weights, int64_t T, int64_t d_out);
+
+/* The projection to queries, keys and values with the head norms and the rotation behind it.
+ * Token t = b * seq + s of x gives row t of y [batch * seq, d_out]: q_heads query heads, then
+ * k_heads key heads, both through the norm and rotation of oq_qk_norm_rope, then the remaining
+ * d_out - (q_heads + k_heads) * head_dim columns (values, or whatever else the projection
+ * yields) as the layer gives them.
+ *   weights      OQ_W_INT8: as oq_linear_w8a8 (INT8 absmax plans); the queries and keys stay
+ *                float32 up to their one rounding. OQ_W_INT4: as oq_linear, whose kernels give
+ *                bf16, so queries and keys are rounded before the norm as well as after it
+ *   w, w_scale, w_rowsum, bias   as for the layer; d_out >= (q_heads + k_heads) * head_dim
+ *   positions, pos_batch_stride  as for oq_qk_norm_rope
+ *   workspace    oq_linear_qkv_workspace_bytes, 256-byte aligned, scratch owned by the caller */
+oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* x_bf16,
+                        int64_t batch, int64_t seq, int64_t ldx, oq_weight_kind weights,
+                        const void* w, const float* w_scale, const float* w_rowsum,
+                        const void* bias_bf16, int64_t d_out, const int32_t* positions,
+                        int64_t pos_batch_stride, void* y_bf16, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* Size in bytes of the library's static scratch array used by oq_linear_static_scratch. */
 #define OQ_STATIC_SCRATCH_BYTES (16u << 20)

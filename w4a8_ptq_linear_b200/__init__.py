@@ -27,6 +27,9 @@ OQ_ERR_CUDA, OQ_ERR_DEVICE_TIMEOUT, OQ_ERR_NOMEM = 4, 5, 6
 ACT_KINDS = {"int8_absmax": 0, "int4_absmax": 1, "int4_lloydmax": 2, "int4_percentile": 3,
              "int4_lloydmax_width": 4, "int8_lloydmax": 5, "int2_percentile": 6}
 OUT_BF16, OUT_ACC = 0, 1
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+ROPES = {"none": 0, "pairs": 1, "halves": 2}
+W_INT4, W_INT8 = 0, 1
 
 # (name, restype, argtypes) of every exported entry point
 _P, _I, _I64, _U64, _SZ, _D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
@@ -59,6 +62,13 @@ SIGNATURES = [
     ("oq_linear_g64", _I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     ("oq_linear_fused", _I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     ("oq_linear_static_scratch", _I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P]),
+    ("oq_prepare_weights_w8", _I, [_P, _P, _I64, _I64, _P, _P, _P, _P]),
+    ("oq_gemm_w8a8", _I, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P]),
+    ("oq_linear_w8a8", _I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    ("oq_qk_norm_rope", _I, [_P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P]),
+    ("oq_linear_qkv_workspace_bytes", _SZ, [_P, _P, _I, _I64, _I64]),
+    ("oq_linear_qkv", _I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _I64, _P, _I64, _P,
+                           _P, _SZ, _P]),
     ("oq_mma_peak_loop", _I, [_I, _I64, _P, _P]),
     ("oq_debug_pair_layout", _I, [_I, _I, _U64, _P]),
 ]
@@ -446,6 +456,256 @@ def linear_static_scratch(plan: Plan, x, w_packed, w_scale, w_rowsum=None, bias=
     _check(lib().oq_linear_static_scratch(plan.handle, _ptr(x), T, x.stride(0), _ptr(w_packed),
                                           _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), N,
                                           _ptr(out), _stream(stream)))
+    return out
+
+
+# ---- INT8 weights and the attention input -----------------------------------------------------
+
+def _need(t, name, dtype, ndim=None):
+    """The tensor's device pointer, or OQError where the library could not read it: another
+    type, on the host or another device, rows that are not contiguous."""
+    import torch
+    if t.dtype != dtype or (ndim is not None and t.dim() != ndim):
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a {ndim}-d {dtype} tensor, got "
+                                          f"{t.dim()}-d {t.dtype}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
+    if not t.is_contiguous():
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _need_vec(t, name, dtype, n):
+    """As _need for an optional vector of n elements (None: NULL)."""
+    if t is None:
+        return None
+    p = _need(t, name, dtype, 1)
+    if t.shape[0] != n:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {t.shape[0]} elements, expected {n}")
+    return p
+
+
+def _need_rows(t, name, d):
+    """Pointer and pitch of a bf16 [T, d] tensor whose rows may lie apart."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != d or (
+            t.shape[1] > 1 and t.stride(1) != 1):
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a bfloat16 [T, {d}] tensor with "
+                                          "contiguous rows")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else d)
+
+
+def _need_out(out, shape, dtype, dev, name="out"):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, name, dtype, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {tuple(out.shape)}, expected {tuple(shape)}")
+    return out
+
+
+def _scratch(workspace, need, dev, stream):
+    """The caller's workspace, or one from torch's allocator that stays in use on `stream`."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise OQError(OQ_ERR_INVALID_ARG, "workspace: must be a contiguous CUDA tensor")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def prepare_weights_w8(plan: Plan, w, *, stream=None):
+    """oq_prepare_weights_w8 on a bf16 [n_out, d] CUDA tensor: (w_codes int8 [n_out, d],
+    w_scale float32 [n_out], w_rowsum float32 [n_out])."""
+    import torch
+    wp, ldw = _need_rows(w, "w", plan.d)
+    n = w.shape[0]
+    codes = torch.empty((n, plan.d), dtype=torch.int8, device=w.device)
+    ws = torch.empty(n, dtype=torch.float32, device=w.device)
+    w1 = torch.empty(n, dtype=torch.float32, device=w.device)
+    _check(lib().oq_prepare_weights_w8(plan.handle, wp, n, ldw, codes.data_ptr(), ws.data_ptr(),
+                                       w1.data_ptr(), _stream(stream)))
+    return codes, ws, w1
+
+
+def gemm_w8a8(a, a_scale, w_codes, w_scale, *, mean=None, w_rowsum=None, bias=None,
+              out_kind=OUT_BF16, out=None, stream=None):
+    """oq_gemm_w8a8: int8 [T, K] codes x int8 [N, K] weights -> bf16 (or int32 sums) [T, N]."""
+    import torch
+    f32 = torch.float32
+    ap, wp = _need(a, "a", torch.int8, 2), _need(w_codes, "w_codes", torch.int8, 2)
+    (T, K), N = a.shape, w_codes.shape[0]
+    if w_codes.shape[1] != K:
+        raise OQError(OQ_ERR_INVALID_ARG, f"a has {K} columns, w_codes {w_codes.shape[1]}")
+    out = _need_out(out, (T, N), torch.bfloat16 if out_kind == OUT_BF16 else torch.int32, a.device)
+    _check(lib().oq_gemm_w8a8(
+        ap, _need_vec(a_scale, "a_scale", f32, T), _need_vec(mean, "mean", f32, T), wp,
+        _need_vec(w_scale, "w_scale", f32, N), _need_vec(w_rowsum, "w_rowsum", f32, N),
+        _need_vec(bias, "bias", torch.bfloat16, N), T, K, N, out_kind, out.data_ptr(),
+        _stream(stream)))
+    return out
+
+
+def linear_w8a8(plan: Plan, x, w_codes, w_scale, w_rowsum=None, bias=None, *, workspace=None,
+                out=None, stream=None):
+    """oq_linear_w8a8: the whole layer against INT8 weights, bf16 [T, d] -> bf16 [T, N]."""
+    import torch
+    f32 = torch.float32
+    xp, ldx = _need_rows(x, "x", plan.d)
+    wp = _need(w_codes, "w_codes", torch.int8, 2)
+    T, N = x.shape[0], w_codes.shape[0]
+    if w_codes.shape[1] != plan.d:
+        raise OQError(OQ_ERR_INVALID_ARG, f"w_codes: {w_codes.shape[1]} columns, plan d={plan.d}")
+    out = _need_out(out, (T, N), torch.bfloat16, x.device)
+    workspace, nbytes = _scratch(workspace, plan.workspace_bytes(T), x.device, stream)
+    _check(lib().oq_linear_w8a8(
+        plan.handle, xp, T, ldx, wp, _need_vec(w_scale, "w_scale", f32, N),
+        _need_vec(w_rowsum, "w_rowsum", f32, N), _need_vec(bias, "bias", torch.bfloat16, N), N,
+        out.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+    return out
+
+
+class _HeadsStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("head_dim", "q_heads", "k_heads", "norm", "rope",
+                                               "rot_dim")]
+                + [("eps", ctypes.c_float)]
+                + [(n, _P) for n in ("q_weight", "q_bias", "k_weight", "k_bias", "cos", "sin")]
+                + [("n_pos", _I64)])
+
+
+class Heads:
+    """The query and key heads of an attention input (oq_heads): their norm ("none", "rms",
+    "layer") with float32 [head_dim] weights and biases, and their rotation ("none", "pairs",
+    "halves") with float32 [n_pos, rot_dim / 2] tables of cosines and sines. It keeps the
+    tensors alive and can be used by any number of calls."""
+
+    def __init__(self, head_dim, q_heads, k_heads, *, norm="rms", eps=1e-6, q_weight=None,
+                 q_bias=None, k_weight=None, k_bias=None, rope="none", cos=None, sin=None):
+        import torch
+        f32 = torch.float32
+        if norm not in NORMS or rope not in ROPES:
+            raise OQError(OQ_ERR_INVALID_ARG, f"unknown norm {norm!r} or rope {rope!r}")
+        self.head_dim, self.q_heads, self.k_heads = head_dim, q_heads, k_heads
+        self._keep = (q_weight, q_bias, k_weight, k_bias, cos, sin)
+        vec = [_need_vec(t, n, f32, head_dim) for t, n in
+               ((q_weight, "q_weight"), (q_bias, "q_bias"), (k_weight, "k_weight"),
+                (k_bias, "k_bias"))]
+        tab, rot, n_pos = [None, None], 0, 0
+        if rope != "none":
+            if cos is None or sin is None or cos.shape != sin.shape:
+                raise OQError(OQ_ERR_INVALID_ARG, "cos and sin: two tables of the same shape")
+            tab = [_need(cos, "cos", f32, 2), _need(sin, "sin", f32, 2)]
+            n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        self.device = next((t.device for t in self._keep if t is not None), None)
+        self._s = _HeadsStruct(head_dim, q_heads, k_heads, NORMS[norm], ROPES[rope], rot, eps,
+                               *vec, *tab, n_pos)
+        self._ref = ctypes.addressof(self._s)
+
+
+_Strides = _I64 * 3
+
+
+def _head_rows(t, name, heads):
+    """(pointer, strides) of a bf16 [B, S, heads.., D] view whose elements are contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() not in (3, 4) or t.stride(-1) != 1:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a bfloat16 [S, heads, head_dim] or "
+                                          "[B, S, heads, head_dim] tensor, elements contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
+    st = t.stride()
+    return t.data_ptr(), _Strides(*(st[:3] if len(st) == 4 else (0, st[0], st[1])))
+
+
+def _positions(positions, B, S):
+    """(pointer, batch stride) of int32 [S] or [B, S] positions."""
+    import torch
+    if positions is None:
+        return None, 0
+    if positions.dim() not in (1, 2) or tuple(positions.shape) not in ((S,), (B, S)):
+        raise OQError(OQ_ERR_INVALID_ARG, f"positions: {tuple(positions.shape)}, expected "
+                                          f"({S},) or ({B}, {S})")
+    return (_need(positions, "positions", torch.int32, positions.dim()),
+            S if positions.dim() == 2 else 0)
+
+
+def _check_heads_device(heads):
+    import torch
+    if heads.device is not None and heads.device.index != torch.cuda.current_device():
+        raise OQError(OQ_ERR_INVALID_ARG, f"heads: its tensors are on {heads.device}, not the "
+                                          "current CUDA device")
+
+
+def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, stream=None):
+    """oq_qk_norm_rope on bf16 [S, heads, head_dim] or [B, S, heads, head_dim] tensors (any
+    strides with contiguous elements; None where there are no such heads). positions: int32 [S]
+    or [B, S], default 0..S-1; a negative one leaves its token unrotated. Returns (q_out, k_out),
+    new contiguous tensors unless given; an output may be its input."""
+    import torch
+    _check_heads_device(heads)
+    io, lead, dev = [], None, None
+    for t, o, name, n in ((q, q_out, "q", heads.q_heads), (k, k_out, "k", heads.k_heads)):
+        if t is None:
+            if n or o is not None:
+                raise OQError(OQ_ERR_INVALID_ARG, f"{name}: missing, with {n} heads")
+            io.append((None, None, None, None, None))
+            continue
+        shape = tuple(t.shape)
+        if shape[-2:] != (n, heads.head_dim) or (lead is not None and shape[:-2] != lead):
+            raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {shape}, expected "
+                                              f"{lead or '[B,] S'} x ({n}, {heads.head_dim})")
+        lead, dev = shape[:-2], t.device
+        ip, ist = _head_rows(t, name, heads)
+        if o is None:
+            o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        elif tuple(o.shape) != shape:
+            raise OQError(OQ_ERR_INVALID_ARG, f"{name}_out: {tuple(o.shape)}, expected {shape}")
+        op, ost = _head_rows(o, name + "_out", heads)
+        io.append((ip, ist, op, ost, o))
+    if lead is None:
+        raise OQError(OQ_ERR_INVALID_ARG, "neither q nor k given")
+    B, S = lead if len(lead) == 2 else (1, lead[0])
+    pos, pbs = _positions(positions, B, S)
+    (qp, qs, qo, qos, q_out), (kp, ks, ko, kos, k_out) = io
+    _check(lib().oq_qk_norm_rope(heads._ref, B, S, qp, qs, kp, ks, pos, pbs, qo, qos, ko, kos,
+                                 _stream(stream)))
+    return q_out, k_out
+
+
+def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None, *, batch=1,
+               positions=None, workspace=None, out=None, stream=None):
+    """oq_linear_qkv: the projection of bf16 [batch * S, d] tokens to [batch * S, N] rows of
+    query heads, key heads (both normed and rotated) and the remaining columns (values). w: int8
+    [N, d] of prepare_weights_w8, or uint8 [N, d/2] of prepare_weights. positions: int32 [S] or
+    [batch, S], as for qk_norm_rope; a [B, S] tensor also sets the batch."""
+    import torch
+    f32 = torch.float32
+    _check_heads_device(heads)
+    xp, ldx = _need_rows(x, "x", plan.d)
+    w8 = w.dtype == torch.int8
+    wp = _need(w, "w", torch.int8 if w8 else torch.uint8, 2)
+    T, N = x.shape[0], w.shape[0]
+    if w.shape[1] != (plan.d if w8 else plan.d // 2):
+        raise OQError(OQ_ERR_INVALID_ARG, f"w: {w.shape[1]} columns for plan d={plan.d}")
+    if positions is not None and positions.dim() == 2:
+        batch = positions.shape[0]
+    if batch < 1 or T % batch:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{T} tokens are not {batch} sequences of one length")
+    S = T // batch
+    pos, pbs = _positions(positions, batch, S)
+    out = _need_out(out, (T, N), torch.bfloat16, x.device)
+    kind = W_INT8 if w8 else W_INT4
+    need = lib().oq_linear_qkv_workspace_bytes(plan.handle, heads._ref, kind, T, N)
+    workspace, nbytes = _scratch(workspace, need, x.device, stream)
+    _check(lib().oq_linear_qkv(
+        plan.handle, heads._ref, xp, batch, S, ldx, kind, wp, _need_vec(w_scale, "w_scale", f32, N),
+        _need_vec(w_rowsum, "w_rowsum", f32, N), _need_vec(bias, "bias", torch.bfloat16, N), N,
+        pos, pbs, out.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
     return out
 
 

@@ -1,5 +1,6 @@
 // C ABI of the rotated, quantized linear layer (declarations and contracts: include/oq.h).
 // Host-side validation, plan lifecycle, the device error word and dispatch to the kernels.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -112,6 +113,76 @@ oq_status check_gemm_args(const void* a, const float* a_scale, const float* mean
     return fail(OQ_ERR_MISALIGNED, "activation, weight and output must be 16-byte aligned");
   (void)bias;
   return OQ_OK;
+}
+
+oq_status check_heads(const oq_heads* h) {
+  if (!h) return fail(OQ_ERR_INVALID_ARG, "NULL heads");
+  if (h->head_dim < 16 || h->head_dim > 256 || h->head_dim % 16)
+    return fail(OQ_ERR_INVALID_ARG, "head_dim=%d must be a multiple of 16 in [16, 256]",
+                h->head_dim);
+  if (h->q_heads < 0 || h->k_heads < 0 || (int64_t)h->q_heads + h->k_heads < 1 ||
+      (int64_t)h->q_heads + h->k_heads > 65536)
+    return fail(OQ_ERR_INVALID_ARG, "q_heads=%d + k_heads=%d must lie in [1, 65536]", h->q_heads,
+                h->k_heads);
+  if (h->norm != OQ_NORM_NONE && h->norm != OQ_NORM_RMS && h->norm != OQ_NORM_LAYER)
+    return fail(OQ_ERR_INVALID_ARG, "unknown norm %d", h->norm);
+  if (!(h->eps >= 0.f && std::isfinite(h->eps)))
+    return fail(OQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (h->rope != OQ_ROPE_NONE && h->rope != OQ_ROPE_PAIRS && h->rope != OQ_ROPE_HALVES)
+    return fail(OQ_ERR_INVALID_ARG, "unknown rope %d", h->rope);
+  if (h->rope != OQ_ROPE_NONE) {
+    if (h->rot_dim < 16 || h->rot_dim > h->head_dim || h->rot_dim % 16)
+      return fail(OQ_ERR_INVALID_ARG, "rot_dim=%d must be a multiple of 16 in [16, head_dim=%d]",
+                  h->rot_dim, h->head_dim);
+    if (!h->cos || !h->sin || h->n_pos < 1)
+      return fail(OQ_ERR_INVALID_ARG, "the rotation needs cos, sin and n_pos >= 1");
+    if (!aligned16(h->cos) || !aligned16(h->sin))
+      return fail(OQ_ERR_MISALIGNED, "cos and sin must be 16-byte aligned");
+  }
+  if (!aligned16(h->q_weight) || !aligned16(h->q_bias) || !aligned16(h->k_weight) ||
+      !aligned16(h->k_bias))
+    return fail(OQ_ERR_MISALIGNED, "norm weights and biases must be 16-byte aligned");
+  return OQ_OK;
+}
+
+// one of q, k (`name`): the pointers and strides of its heads
+oq_status check_head_io(const char* name, int heads, int64_t batch, int64_t seq, const void* in,
+                        const int64_t* si, const void* out, const int64_t* so) {
+  if (heads == 0 || batch == 0 || seq == 0) return OQ_OK;
+  if (!in || !out || !si || !so)
+    return fail(OQ_ERR_INVALID_ARG, "NULL %s pointer or strides with %d heads", name, heads);
+  if (!aligned16(in) || !aligned16(out))
+    return fail(OQ_ERR_MISALIGNED, "%s and its output must be 16-byte aligned", name);
+  const int64_t n[3] = {batch, seq, heads};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;   // a stride that nothing is multiplied with
+    if (si[i] < 0 || so[i] < 0) return fail(OQ_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (si[i] % 8 || so[i] % 8)
+      return fail(OQ_ERR_MISALIGNED, "%s: strides must be multiples of 8 elements", name);
+    if (so[i] == 0)
+      return fail(OQ_ERR_INVALID_ARG, "%s: the output repeats an element (stride 0)", name);
+  }
+  return OQ_OK;
+}
+
+oq_status check_positions(const int32_t* positions, int64_t pos_batch_stride) {
+  if (positions && pos_batch_stride < 0)
+    return fail(OQ_ERR_INVALID_ARG, "negative pos_batch_stride");
+  if (reinterpret_cast<uintptr_t>(positions) & 3u)
+    return fail(OQ_ERR_MISALIGNED, "positions must be 4-byte aligned");
+  return OQ_OK;
+}
+
+// the part of a launch that does not depend on where the heads lie
+HeadArgs head_args(const oq_heads* h, int64_t batch, int64_t seq, const int32_t* positions,
+                   int64_t pos_batch_stride) {
+  HeadArgs a;
+  a.q.weight = h->q_weight; a.q.bias = h->q_bias; a.q.heads = h->q_heads;
+  a.k.weight = h->k_weight; a.k.bias = h->k_bias; a.k.heads = h->k_heads;
+  a.batch = batch; a.seq = seq; a.head_dim = h->head_dim; a.norm = h->norm; a.rope = h->rope;
+  a.rot_dim = h->rot_dim; a.eps = h->eps; a.cos = h->cos; a.sin = h->sin; a.n_pos = h->n_pos;
+  a.positions = positions; a.pos_batch_stride = pos_batch_stride;
+  return a;
 }
 
 }  // namespace
@@ -714,6 +785,188 @@ oq_status oq_linear_g64(const oq_plan* plan, const void* x_bf16, int64_t T, int6
   return oq_gemm_w4a4_g64(plan->act, ws, scale, plan->center ? mean : nullptr, w_packed, w_sz,
                           w_scale, w_rowsum, bias_bf16, T, plan->d, d_out, OQ_OUT_BF16, y_bf16,
                           stream);
+}
+
+oq_status oq_prepare_weights_w8(const oq_plan* plan, const void* w_bf16, int64_t n_out,
+                                int64_t ldw, int8_t* w_codes, float* w_scale, float* w_rowsum,
+                                void* stream) {
+  if (!plan) return fail(OQ_ERR_INVALID_ARG, "NULL plan");
+  if (n_out < 0 || n_out > 0x7FFFFFFF) return fail(OQ_ERR_INVALID_ARG, "n_out out of range");
+  if (ldw < plan->d || (ldw * 2) % 16) return fail(OQ_ERR_MISALIGNED, "ldw must be >= d and a multiple of 8");
+  if (n_out > 0 && (!w_bf16 || !w_codes || !w_scale || !w_rowsum))
+    return fail(OQ_ERR_INVALID_ARG, "NULL weight argument");
+  if (!aligned16(w_bf16) || !aligned16(w_codes))
+    return fail(OQ_ERR_MISALIGNED, "w and w_codes must be 16-byte aligned");
+  oq_status st = check_plan_device(plan);
+  if (st != OQ_OK) return st;
+  return rotate_quantize_impl(plan, w_bf16, n_out, ldw, w_codes, w_scale, nullptr, nullptr,
+                              w_rowsum, kRqInt8, 0, 0, static_cast<cudaStream_t>(stream));
+}
+
+oq_status oq_gemm_w8a8(const int8_t* a, const float* a_scale, const float* mean,
+                       const int8_t* w_codes, const float* w_scale, const float* w_rowsum,
+                       const void* bias_bf16, int64_t T, int64_t d_in, int64_t d_out,
+                       oq_out_kind out_kind, void* out, void* stream) {
+  oq_status st = check_gemm_args(a, a_scale, mean, reinterpret_cast<const uint8_t*>(w_codes),
+                                 w_scale, w_rowsum, bias_bf16, T, d_in, d_out, (int)out_kind,
+                                 T == 0 && !out ? w_codes : out);   // no token: no output needed
+  if (st != OQ_OK) return st;
+  GemmW8Args g;
+  g.a = a; g.a_scale = a_scale; g.mean = mean; g.w = w_codes; g.w_scale = w_scale;
+  g.w_rowsum = w_rowsum; g.bias = bias_bf16; g.T = T; g.K = d_in; g.N = d_out;
+  g.out_acc = out_kind == OQ_OUT_ACC; g.out = out;
+  return launch_gemm_w8(g, static_cast<cudaStream_t>(stream));
+}
+
+// The INT8-weight layer; with `head` the first n_head columns go there in float32.
+static oq_status linear_w8a8_impl(const oq_plan* plan, const void* x, int64_t T, int64_t ldx,
+                                  const int8_t* w, const float* w_scale, const float* w_rowsum,
+                                  const void* bias, int64_t d_out, void* y, void* workspace,
+                                  float* head, int64_t n_head, void* stream) {
+  const size_t code_bytes = linear_code_bytes(plan, T);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* scale = reinterpret_cast<float*>(ws + round256(code_bytes));
+  float* mean = reinterpret_cast<float*>(ws + round256(code_bytes) + round256((size_t)T * 4));
+  // every argument of both steps is checked before the first is launched
+  oq_status st = check_gemm_args(ws, scale, plan->center ? mean : nullptr,
+                                 reinterpret_cast<const uint8_t*>(w), w_scale, w_rowsum, bias, T,
+                                 plan->d, d_out, OQ_OUT_BF16,
+                                 T == 0 && !y ? static_cast<const void*>(w) : y);
+  if (st != OQ_OK) return st;
+  st = oq_rotate_quantize(plan, x, T, ldx, ws, scale, mean, nullptr, stream);
+  if (st != OQ_OK) return st;
+  GemmW8Args g;
+  g.a = reinterpret_cast<const int8_t*>(ws); g.a_scale = scale;
+  g.mean = plan->center ? mean : nullptr;
+  g.w = w; g.w_scale = w_scale; g.w_rowsum = w_rowsum; g.bias = bias; g.T = T; g.K = plan->d;
+  g.N = d_out; g.out = y; g.head = head; g.n_head = n_head;
+  return launch_gemm_w8(g, static_cast<cudaStream_t>(stream));
+}
+
+// what oq_linear_w8a8 and oq_linear_qkv check of the layer before anything is launched
+static oq_status check_layer(const oq_plan* plan, int64_t T, const float* w_rowsum,
+                             const void* workspace, size_t workspace_bytes, size_t need) {
+  if (T < 0 || T > 0x7FFFFFFF) return fail(OQ_ERR_INVALID_ARG, "T out of range");
+  if (T > 0 && (!workspace || workspace_bytes < need))
+    return fail(OQ_ERR_INVALID_ARG, "workspace too small: need %zu bytes", need);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(OQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (plan->center && !w_rowsum) return fail(OQ_ERR_INVALID_ARG, "centering needs w_rowsum");
+  return OQ_OK;
+}
+
+oq_status oq_linear_w8a8(const oq_plan* plan, const void* x_bf16, int64_t T, int64_t ldx,
+                         const int8_t* w_codes, const float* w_scale, const float* w_rowsum,
+                         const void* bias_bf16, int64_t d_out, void* y_bf16, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!plan) return fail(OQ_ERR_INVALID_ARG, "NULL plan");
+  if (plan->act != OQ_ACT_INT8_ABSMAX)
+    return fail(OQ_ERR_INVALID_ARG, "INT8 weights need an INT8_ABSMAX plan");
+  oq_status st = check_layer(plan, T, w_rowsum, workspace, workspace_bytes,
+                             oq_linear_workspace_bytes(plan, T));
+  if (st != OQ_OK) return st;
+  return linear_w8a8_impl(plan, x_bf16, T, ldx, w_codes, w_scale, w_rowsum, bias_bf16, d_out,
+                          y_bf16, workspace, nullptr, 0, stream);
+}
+
+oq_status oq_qk_norm_rope(const oq_heads* heads, int64_t batch, int64_t seq, const void* q,
+                          const int64_t q_strides[3], const void* k, const int64_t k_strides[3],
+                          const int32_t* positions, int64_t pos_batch_stride, void* q_out,
+                          const int64_t q_out_strides[3], void* k_out,
+                          const int64_t k_out_strides[3], void* stream) {
+  oq_status st = check_heads(heads);
+  if (st != OQ_OK) return st;
+  if (batch < 0 || seq < 0 || (seq > 0 && batch > 0x7FFFFFFF / seq))
+    return fail(OQ_ERR_INVALID_ARG, "batch=%lld x seq=%lld out of range", (long long)batch,
+                (long long)seq);
+  st = check_head_io("q", heads->q_heads, batch, seq, q, q_strides, q_out, q_out_strides);
+  if (st != OQ_OK) return st;
+  st = check_head_io("k", heads->k_heads, batch, seq, k, k_strides, k_out, k_out_strides);
+  if (st != OQ_OK) return st;
+  st = check_positions(positions, pos_batch_stride);
+  if (st != OQ_OK) return st;
+  HeadArgs a = head_args(heads, batch, seq, positions, pos_batch_stride);
+  auto place = [](HeadIo& io, const void* in, const int64_t* si, void* out, const int64_t* so) {
+    io.in = in;
+    io.out = out;
+    for (int i = 0; io.heads && i < 3; ++i) io.si[i] = si[i], io.so[i] = so[i];
+  };
+  if (batch > 0 && seq > 0) {
+    place(a.q, q, q_strides, q_out, q_out_strides);
+    place(a.k, k, k_strides, k_out, k_out_strides);
+  }
+  return launch_heads(a, static_cast<cudaStream_t>(stream));
+}
+
+// float32 query and key columns of the INT8 projection, behind the layer's own workspace
+static size_t head_bytes(const oq_heads* h, oq_weight_kind weights, int64_t T) {
+  return weights == OQ_W_INT8
+             ? round256((size_t)T * (size_t)(h->q_heads + h->k_heads) * h->head_dim * 4)
+             : 0;
+}
+
+size_t oq_linear_qkv_workspace_bytes(const oq_plan* plan, const oq_heads* heads,
+                                     oq_weight_kind weights, int64_t T, int64_t d_out) {
+  (void)d_out;
+  if (!plan || T < 0 || T > 0x7FFFFFFF || check_heads(heads) != OQ_OK) return 0;
+  return oq_linear_workspace_bytes(plan, T) + head_bytes(heads, weights, T);
+}
+
+oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* x_bf16,
+                        int64_t batch, int64_t seq, int64_t ldx, oq_weight_kind weights,
+                        const void* w, const float* w_scale, const float* w_rowsum,
+                        const void* bias_bf16, int64_t d_out, const int32_t* positions,
+                        int64_t pos_batch_stride, void* y_bf16, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!plan) return fail(OQ_ERR_INVALID_ARG, "NULL plan");
+  oq_status st = check_heads(heads);
+  if (st != OQ_OK) return st;
+  if (batch < 0 || seq < 0 || (seq > 0 && batch > 0x7FFFFFFF / seq))
+    return fail(OQ_ERR_INVALID_ARG, "batch=%lld x seq=%lld out of range", (long long)batch,
+                (long long)seq);
+  if (weights != OQ_W_INT4 && weights != OQ_W_INT8)
+    return fail(OQ_ERR_INVALID_ARG, "unknown weight kind %d", (int)weights);
+  if (weights == OQ_W_INT8 && plan->act != OQ_ACT_INT8_ABSMAX)
+    return fail(OQ_ERR_INVALID_ARG, "INT8 weights need an INT8_ABSMAX plan");
+  const int64_t T = batch * seq;
+  const int64_t nq = (int64_t)heads->q_heads * heads->head_dim;
+  const int64_t n_head = nq + (int64_t)heads->k_heads * heads->head_dim;
+  if (d_out < n_head)
+    return fail(OQ_ERR_INVALID_ARG, "d_out=%lld holds fewer than the %lld query and key columns",
+                (long long)d_out, (long long)n_head);
+  st = check_layer(plan, T, w_rowsum, workspace, workspace_bytes,
+                   oq_linear_qkv_workspace_bytes(plan, heads, weights, T, d_out));
+  if (st != OQ_OK) return st;
+  st = check_positions(positions, pos_batch_stride);
+  if (st != OQ_OK) return st;
+  if (T == 0) return OQ_OK;
+  if (!y_bf16 || !aligned16(y_bf16))
+    return fail(y_bf16 ? OQ_ERR_MISALIGNED : OQ_ERR_INVALID_ARG, "y must be given, 16-byte aligned");
+  const size_t layer = oq_linear_workspace_bytes(plan, T);
+  float* head = weights == OQ_W_INT8
+                    ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + layer) : nullptr;
+  if (weights == OQ_W_INT8)
+    st = linear_w8a8_impl(plan, x_bf16, T, ldx, static_cast<const int8_t*>(w), w_scale, w_rowsum,
+                          bias_bf16, d_out, y_bf16, workspace, head, n_head, stream);
+  else
+    st = oq_linear(plan, x_bf16, T, ldx, static_cast<const uint8_t*>(w), w_scale, w_rowsum,
+                   bias_bf16, d_out, y_bf16, workspace, layer, stream);
+  if (st != OQ_OK) return st;
+  HeadArgs a = head_args(heads, batch, seq, positions, pos_batch_stride);
+  const int64_t ld = head ? n_head : d_out;
+  const int esz = head ? 4 : 2;
+  a.in_f32 = head != nullptr;
+  const uint8_t* src = head ? reinterpret_cast<const uint8_t*>(head)
+                            : static_cast<const uint8_t*>(y_bf16);
+  a.q.in = src;
+  a.k.in = src + nq * esz;
+  a.q.out = y_bf16;
+  a.k.out = static_cast<uint8_t*>(y_bf16) + nq * 2;
+  for (HeadIo* io : {&a.q, &a.k}) {
+    io->si[0] = seq * ld; io->si[1] = ld; io->si[2] = heads->head_dim;
+    io->so[0] = seq * d_out; io->so[1] = d_out; io->so[2] = heads->head_dim;
+  }
+  return launch_heads(a, static_cast<cudaStream_t>(stream));
 }
 
 oq_status oq_debug_wait_timeout(uint64_t timeout_ns, void* stream) {
