@@ -10,11 +10,9 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <cstring>
 #include <map>
 #include <mutex>
-#include <tuple>
-#include <vector>
+#include <utility>
 
 #include "oq_internal.h"
 #include "ptx.cuh"
@@ -36,6 +34,7 @@ struct W8Params {
   const float* w_rowsum;
   const __nv_bfloat16* bias;
   int T, K, N, out_acc, n_head;
+  bool wide;                // out is 32-byte aligned (its rows are: N % 16 == 0)
   void* out;
   float* head;
   unsigned long long* err;
@@ -56,64 +55,110 @@ struct W8Params {
 // What bounds it: a 256 x 256 tile reads 64 KB per 128 bytes of K for 2 * 256 * 256 * 128 operations,
 // 64 bytes a clock and SM at the tensor pipe's full rate, which is about what L2 delivers.
 //
-// Schedule: a pair takes a contiguous range of the (token block, channel chunk) space, cut into
-// tiles of at most 256 channels. A tile costs its chunks and, whatever its width, the 128 token rows
-// of each CTA, so the ranges are chosen by a cost of chunks plus a fixed part per tile.
+// Schedule: tiles in waves, one to a pair, down the token blocks of a group first, so that the
+// tiles in flight share their weights and the group's activations stay in L2 (ranges of tiles
+// contiguous in a token block kept all weights live at once and took 154 us instead of XX at 4096 x
+// 4096 x 12288). What does not fill a wave is cut into narrower tiles, one to a pair.
 constexpr int TM = 128;                    // tokens per CTA
 constexpr int TN = 256;                    // channels per tile at most
-constexpr int CH = 32;                     // channels per chunk
-constexpr int SK = 6;                      // stages of one 128-byte K block
-constexpr int AB = TM * 128;               // activation bytes of a stage
-constexpr int BB = (TN / 2) * 128;         // weight bytes of a stage (this CTA's half)
+constexpr int CH = 64;                     // channels per chunk
+constexpr int KS = 2;                      // 128-byte K blocks per stage
+constexpr int SK = 3;                      // stages
+constexpr int AK = TM * 128;               // activation bytes of a K block
+constexpr int BK = (TN / 2) * 128;         // weight bytes of a K block (this CTA's half)
+constexpr int AB = KS * AK, BB = KS * BK;  // of a stage
 constexpr int BBOX = 64;                   // weight rows of one TMA load
 constexpr int NEPI = 256;                  // epilogue threads, two warps to a TMEM lane quarter
 constexpr int NTHR = 128 + NEPI;
-constexpr int STG = 32 * 64;               // staging tile: 32 tokens x 64 bytes
 constexpr int OFF_B = SK * AB;
-constexpr int OFF_STG = OFF_B + SK * BB;
-constexpr int OFF_COL = OFF_STG + (NEPI / 32) * STG;   // [2][3][TN] floats
+constexpr int OFF_COL = OFF_B + SK * BB;   // [2][3][TN] floats
 constexpr int OFF_BAR = OFF_COL + 2 * 3 * TN * 4;
 constexpr int NBAR = 2 * SK + 5;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
-constexpr int kMaxUnits = 96;              // CTA pairs at most
 static_assert(SMEM <= 232448, "shared memory");
 
 struct TileParams {
   W8Params w;
   int npm;                                 // chunks of a token block
-  int sched[kMaxUnits + 1];                // pair u: chunks [sched[u], sched[u + 1])
+  int blocks, ncol, gm;                    // token blocks, tiles of a block, blocks of a group
+  int total, full;                         // tiles; those run whole
+  int split;                               // parts that each of the others is cut into
 };
 
-// The tiles of one pair's range; every role walks the same sequence.
+// The tiles of one pair, the same sequence in every role: pair u takes tiles u, u + units, ...
+// whole, as long as there is one for every pair, then at most one part of a remaining tile.
 struct Tiles {
-  int npm, maxch, cur, end;
-  __device__ Tiles(const TileParams& p, int unit, int maxch_)
-      : npm(p.npm), maxch(maxch_), cur(p.sched[unit]), end(p.sched[unit + 1]) {}
+  const TileParams& p;
+  int idx, units;
+  __device__ Tiles(const TileParams& p_, int unit, int units_) : p(p_), idx(unit), units(units_) {}
   // token block m, first chunk c0, number of chunks n
   __device__ bool next(int& m, int& c0, int& n) {
-    if (cur >= end) return false;
-    m = cur / npm;
-    c0 = cur - m * npm;
-    const int left = min(end, (m + 1) * npm) - cur;
-    const int cuts = (left + maxch - 1) / maxch;
-    n = (left + cuts - 1) / cuts;
-    cur += n;
-    return true;
+    int tile = idx, part = 0;
+    const bool whole = idx < p.full;
+    if (!whole) {
+      tile = p.full + (idx - p.full) / p.split;
+      part = (idx - p.full) % p.split;
+    }
+    if (tile >= p.total) return false;
+    idx += units;
+    const int g = tile / (p.gm * p.ncol), r = tile - g * p.gm * p.ncol;
+    const int rows = min(p.gm, p.blocks - g * p.gm);
+    const int col = r / rows;
+    m = g * p.gm + r - col * rows;
+    c0 = (int)((int64_t)col * p.npm / p.ncol);
+    n = (int)((int64_t)(col + 1) * p.npm / p.ncol) - c0;
+    if (!whole) {
+      const int a = part * n / p.split, b = (part + 1) * n / p.split;
+      c0 += a;
+      n = b - a;
+    }
+    return n > 0;
   }
 };
 
-// y of two neighbouring channels: c = fma(mean, w1, b), y = fma(acc, alpha s, c)
-__device__ __forceinline__ float2 dequant2(int a0, int a1, float alpha, float mean, float2 s,
-                                           float2 w1, float2 b) {
-  const float2 c = __ffma2_rn(make_float2(mean, mean), w1, b);
-  return __ffma2_rn(make_float2((float)a0, (float)a1),
-                    __fmul2_rn(make_float2(alpha, alpha), s), c);
+// 32 bytes from registers; `wide`: the address is a multiple of 32
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* d = reinterpret_cast<uint4*>(dst);
+    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float2 y) {
+  const __nv_bfloat162 v = __float22bfloat162_rn(y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// y of a token's 32 neighbouring channels: c = fma(mean, w1, b), y = fma(acc, alpha s, c). The
+// channels' constants lie at cs (scales), cs + TN (row sums) and cs + 2 TN (biases) floats, the last
+// two read only where they count: shared memory is what the mainloop is short of.
+__device__ __forceinline__ void dequant32(const uint32_t (&r)[32], float alpha, float mean,
+                                          const float4* cs, bool has_mean, bool has_bias,
+                                          float2 (&y)[16]) {
+  const float2 al = make_float2(alpha, alpha), mn = make_float2(mean, mean);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float4 w4 = make_float4(0.f, 0.f, 0.f, 0.f), b4 = w4;
+    const float4 s4 = cs[i];
+    if (has_mean) w4 = cs[TN / 4 + i];
+    if (has_bias) b4 = cs[TN / 2 + i];
+    const float2 c0 = __ffma2_rn(mn, make_float2(w4.x, w4.y), make_float2(b4.x, b4.y));
+    const float2 c1 = __ffma2_rn(mn, make_float2(w4.z, w4.w), make_float2(b4.z, b4.w));
+    y[2 * i] = __ffma2_rn(make_float2((float)(int)r[4 * i], (float)(int)r[4 * i + 1]),
+                          __fmul2_rn(al, make_float2(s4.x, s4.y)), c0);
+    y[2 * i + 1] = __ffma2_rn(make_float2((float)(int)r[4 * i + 2], (float)(int)r[4 * i + 3]),
+                              __fmul2_rn(al, make_float2(s4.z, s4.w)), c1);
+  }
 }
 
 __global__ void __launch_bounds__(NTHR, 1)
     k_gemm_w8(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-              const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_h,
               const __grid_constant__ TileParams tp) {
   const W8Params& p = tp.w;
   extern __shared__ uint8_t smem_raw[];
@@ -128,6 +173,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   const uint32_t rank = dev::cluster_ctarank();
   const int unit = (int)blockIdx.x / 2;
   const int nkb = (p.K + 127) / 128;
+  const int nst = (nkb + KS - 1) / KS;   // stages of a tile
   auto bar = [&](int i) { return dev::smem_u32(&bars[i]); };
   auto full_bar = [&](int s) { return bar(s); };
   auto free_bar = [&](int s) { return bar(SK + s); };
@@ -160,7 +206,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   dev::cluster_sync();   // barrier inits of both CTAs visible before any remote arrive
   dev::tc_fence_after();
   const uint32_t tmem = s_misc[0];
-  Tiles it(tp, unit, TN / CH);
+  Tiles it(tp, unit, (int)gridDim.x / 2);
   int m, c0, nch;
 
   if (warp == 0 || warp == 2) {
@@ -172,24 +218,27 @@ __global__ void __launch_bounds__(NTHR, 1)
       while (ok && it.next(m, c0, nch)) {
         const int rows = nch * CH / 2;                      // this CTA's weight rows
         const int boxes = tok ? 1 : (rows + BBOX - 1) / BBOX;
-        const uint32_t bytes = tok ? 2u * AB : 2u * boxes * BBOX * 128u;   // of both CTAs
+        const uint32_t block_bytes = tok ? 2u * AK : 2u * boxes * BBOX * 128u;   // of both CTAs
         const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * CH + (int)rank * rows;
-        for (int kb = 0; kb < nkb; ++kb, ++j) {
-          const int s = j % SK;
+        for (int st = 0; st < nst; ++st, ++j) {
+          const int s = j % SK, nk = min(KS, nkb - st * KS);
           if (!dev::mbar_wait(free_bar(s), ((j / SK) & 1u) ^ 1u, p.err, kSiteGemmEmpty,
                               p.limit_ns) || *s_abort) {
             give_up();
             ok = false;
             break;
           }
-          if (rank == 0) dev::mbar_arrive_expect_tx(full_bar(s), bytes);
-          if (tok)
-            dev::tma_load_2d_pair(dev::smem_u32(smem + s * AB), &tm_a, kb * 128, row0,
-                                  lead(full_bar(s)));
-          else
-            for (int i = 0; i < boxes; ++i)
-              dev::tma_load_2d_pair(dev::smem_u32(smem + OFF_B + s * BB + i * BBOX * 128), &tm_b,
-                                    kb * 128, row0 + i * BBOX, lead(full_bar(s)));
+          if (rank == 0) dev::mbar_arrive_expect_tx(full_bar(s), (uint32_t)nk * block_bytes);
+          for (int u = 0; u < nk; ++u) {
+            const int k = (st * KS + u) * 128;
+            if (tok)
+              dev::tma_load_2d_pair(dev::smem_u32(smem + s * AB + u * AK), &tm_a, k, row0,
+                                    lead(full_bar(s)));
+            else
+              for (int i = 0; i < boxes; ++i)
+                dev::tma_load_2d_pair(dev::smem_u32(smem + OFF_B + s * BB + u * BK + i * BBOX * 128),
+                                      &tm_b, k, row0 + i * BBOX, lead(full_bar(s)));
+          }
         }
       }
       // Every stage this thread filled has been read by its MMAs before the CTA ends (their
@@ -218,8 +267,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         dev::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)(b * TN);
-        for (int kb = 0; kb < nkb; ++kb, ++j) {
-          const int s = j % SK;
+        for (int st = 0; st < nst; ++st, ++j) {
+          const int s = j % SK, nk = min(KS, nkb - st * KS);
           if (!dev::mbar_wait(full_bar(s), (j / SK) & 1u, p.err, kSiteGemmFull, p.limit_ns)) {
             give_up();
             ok = false;
@@ -228,9 +277,14 @@ __global__ void __launch_bounds__(NTHR, 1)
           dev::tc_fence_after();
           const uint32_t sa = dev::smem_u32(smem + s * AB), sb = dev::smem_u32(smem + OFF_B + s * BB);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            dev::mma_i8_pair(dt, dev::sdesc_sw128(sa + kk * 32), dev::sdesc_sw128(sb + kk * 32),
-                             idesc, (kb | kk) != 0);
+          for (int u = 0; u < KS; ++u) {
+            if (u >= nk) break;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              dev::mma_i8_pair(dt, dev::sdesc_sw128(sa + u * AK + kk * 32),
+                               dev::sdesc_sw128(sb + u * BK + kk * 32), idesc,
+                               (st | u | kk) != 0);
+          }
           issued = true;
           dev::mma_commit_pair(free_bar(s));
         }
@@ -245,7 +299,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   } else if (warp >= 4) {
     // ---------------- epilogue: a lane holds a token ----------------
     const int etid = tid - 128, q = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* stg = smem + OFF_STG + (warp - 4) * STG;
     uint32_t n = 0;
     bool ok = true;
     for (; ok && it.next(m, c0, nch); ++n) {
@@ -275,77 +328,36 @@ __global__ void __launch_bounds__(NTHR, 1)
       dev::tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
 #pragma unroll 1
-      for (int c = half; ok && c < nch; c += 2) {
+      for (int c = half; ok && c < nch * (CH / 32); c += 2) {
         uint32_t r[32];
         dev::tmem_ld32(acc + (uint32_t)(c * 32), r);
         dev::tmem_wait_ld();
         const int o = o0 + c * 32;
-        if (tw >= p.T || o >= p.N) continue;
-        // 64-byte rows of the staging tile: 16-byte chunk i of row l at i ^ ((l >> 1) & 3)
-        auto put = [&](int piece, const uint32_t (&v)[4]) {
-          *reinterpret_cast<uint4*>(stg + lane * 64 + ((piece ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
-        };
-        auto begin = [&]() {   // the store before has read its values
-          if (lane == 0) dev::bulk_wait_all_read();
-          __syncwarp();
-        };
-        auto send = [&](const CUtensorMap* map, int x) {
-          dev::fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            dev::tma_store_2d(map, dev::smem_u32(stg), x, tw);
-            dev::bulk_commit();
-          }
-        };
+        if (t >= p.T || o >= p.N) continue;   // no warp-wide step below
+        const bool two = o + 16 < p.N;        // N % 16 == 0: sixteen or all of the channels
         if (p.out_acc) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            begin();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              put(i, {r[h * 16 + 4 * i], r[h * 16 + 4 * i + 1], r[h * 16 + 4 * i + 2],
-                      r[h * 16 + 4 * i + 3]});
-            send(&tm_y, o + h * 16);
-          }
-          continue;
-        }
-        const float2* cs = reinterpret_cast<const float2*>(col + c * 32);
-        float2 y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          y[i] = dequant2((int)r[2 * i], (int)r[2 * i + 1], alpha, mean, cs[i], cs[TN / 2 + i],
-                          cs[TN + i]);
-        auto pack = [&](int i) {
-          const __nv_bfloat162 v = __float22bfloat162_rn(y[i]);
-          return *reinterpret_cast<const uint32_t*>(&v);
-        };
-        if (o >= p.n_head) {
-          begin();
+          int32_t* dst = reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            put(i, {pack(4 * i), pack(4 * i + 1), pack(4 * i + 2), pack(4 * i + 3)});
-          send(&tm_y, o);
-        } else {
-          // float32 columns, 16 to a store; n_head % 16 == 0, so each half is one kind
+            if (i < 2 || two) store32(dst + 8 * i, r + 8 * i, p.wide);
+          continue;
+        }
+        float2 y[16];
+        const float4* cs = reinterpret_cast<const float4*>(col + c * 32);
+        dequant32(r, alpha, mean, cs, p.mean != nullptr, p.bias != nullptr, y);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int oh = o + h * 16;
-            if (oh < p.n_head) {
-              begin();
+        for (int h = 0; h < 2; ++h) {
+          const int oh = o + h * 16;
+          if (h && !two) break;
+          if (oh < p.n_head) {   // n_head % 16 == 0
+            float* dst = p.head + (int64_t)t * p.n_head + oh;
+            store32(dst, reinterpret_cast<const uint32_t*>(y + h * 8), true);
+            store32(dst + 8, reinterpret_cast<const uint32_t*>(y + h * 8 + 4), true);
+          } else {
+            uint32_t v[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                put(i, {__float_as_uint(y[h * 8 + 2 * i].x), __float_as_uint(y[h * 8 + 2 * i].y),
-                        __float_as_uint(y[h * 8 + 2 * i + 1].x),
-                        __float_as_uint(y[h * 8 + 2 * i + 1].y)});
-              send(&tm_h, oh);
-            } else if (t < p.T && oh < p.N) {
-              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                                    (int64_t)t * p.N + oh);
-              dst[0] = make_uint4(pack(h * 8), pack(h * 8 + 1), pack(h * 8 + 2), pack(h * 8 + 3));
-              dst[1] = make_uint4(pack(h * 8 + 4), pack(h * 8 + 5), pack(h * 8 + 6),
-                                  pack(h * 8 + 7));
-            }
+            for (int i = 0; i < 8; ++i) v[i] = pack2(y[h * 8 + i]);
+            store32(reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t * p.N + oh, v, p.wide);
           }
         }
       }
@@ -353,7 +365,6 @@ __global__ void __launch_bounds__(NTHR, 1)
       __syncwarp();
       if (lane == 0) dev::mbar_arrive_cluster(lead(tempty_bar(b)));
     }
-    if (lane == 0) dev::bulk_wait_all();
   }
 
   __syncwarp();
@@ -363,57 +374,6 @@ __global__ void __launch_bounds__(NTHR, 1)
     dev::tc_fence_after();
     dev::tmem_dealloc_pair(tmem, 2 * TN);
   }
-}
-
-// Ranges of the flattened (token block, chunk) space: the largest cost over the pairs, chunks plus
-// kTileCost for every tile of at most maxch chunks inside one token block, is made as small as
-// possible: bisection on the bound, each pair taking as much as the bound allows. kTileCost = 8
-// chunks: a tile reads its token rows whatever its width, as many bytes as 8 chunks of weights.
-// Kept per shape; a space of very many chunks is cut evenly (its tail is short beside it).
-constexpr int kTileCost = 8;
-
-bool make_schedule(int64_t blocks, int npm, int units, int maxch, int* out) {
-  const int64_t total = blocks * npm;
-  if (total > 0x7FFFFFFF) return false;
-  if (total > (1 << 18)) {
-    for (int u = 0; u <= units; ++u) out[u] = (int)(total * u / units);
-    return true;
-  }
-  static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int>, std::vector<int>> kept;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple((int)blocks, npm, units, maxch);
-  auto found = kept.find(key);
-  if (found == kept.end()) {
-    std::vector<int> v((size_t)units + 1);
-    auto fits = [&](int64_t bound) {
-      int64_t pos = 0;
-      for (int u = 0; u < units; ++u) {
-        v[(size_t)u] = (int)pos;
-        int64_t left = bound;
-        while (pos < total) {
-          // whole tiles of the rest of this token block, then a part of one
-          const int64_t run = std::min<int64_t>(npm - pos % npm, maxch);
-          const int64_t take = std::min<int64_t>(run, left - kTileCost);
-          if (take < 1) break;
-          pos += take;
-          left -= take + kTileCost;
-          if (take < run) break;
-        }
-      }
-      v[(size_t)units] = (int)total;
-      return pos >= total;
-    };
-    int64_t lo = 1 + kTileCost, hi = total * (1 + kTileCost);
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (fits(mid)) hi = mid; else lo = mid + 1;
-    }
-    fits(lo);
-    found = kept.emplace(key, std::move(v)).first;
-  }
-  std::copy(found->second.begin(), found->second.end(), out);
-  return true;
 }
 
 // CTA pairs that are resident at once, per kernel and device (0 if the query fails).
@@ -446,35 +406,33 @@ int resident_pairs(const void* kern, int smem, int threads) {
 }
 
 oq_status run_tiles(const W8Params& w, cudaStream_t s) {
-  CUtensorMap ta, tb, ty, th;
-  std::memset(&th, 0, sizeof(th));
+  CUtensorMap ta, tb;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
-  bool ok = tma_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.a, K, T, K, 128, TM,
-                       CU_TENSOR_MAP_SWIZZLE_128B) &&
-            tma_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, BBOX,
-                       CU_TENSOR_MAP_SWIZZLE_128B);
-  if (w.out_acc)
-    ok = ok && tma_map_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_INT32, w.out, N, T, N * 4, 16, 32,
-                          CU_TENSOR_MAP_SWIZZLE_64B);
-  else
-    ok = ok && tma_map_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.out, N, T, N * 2, 32, 32,
-                          CU_TENSOR_MAP_SWIZZLE_64B);
-  if (w.n_head)
-    ok = ok && tma_map_2d(&th, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, w.head, (uint64_t)w.n_head, T,
-                          (uint64_t)w.n_head * 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  const bool ok = tma_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.a, K, T, K, 128, TM,
+                             CU_TENSOR_MAP_SWIZZLE_128B) &&
+                  tma_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, BBOX,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return fail(OQ_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable");
   const auto kern = &k_gemm_w8;
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8)");
   int units = resident_pairs(reinterpret_cast<const void*>(kern), SMEM, NTHR);
   if (units <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no CTA pair fits on this device");
-  TileParams p;
+  TileParams p{};
   p.w = w;
   p.npm = (w.N + CH - 1) / CH;
   const int64_t blocks = ((int64_t)w.T + 2 * TM - 1) / (2 * TM);
-  units = (int)std::min<int64_t>(std::min(units, kMaxUnits), blocks * p.npm);
-  if (!make_schedule(blocks, p.npm, units, TN / CH, p.sched))
+  p.ncol = (p.npm * CH + TN - 1) / TN;
+  if (blocks * p.ncol > 0x3FFFFFFF)
     return fail(OQ_ERR_INVALID_ARG, "gemm_w8: T x d_out too large for one call");
+  p.blocks = (int)blocks;
+  p.total = (int)blocks * p.ncol;
+  // a group's activations take a quarter of L2 at most
+  p.gm = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, (32 << 20) / (2 * TM * (int64_t)w.K)));
+  p.full = p.total / units * units;
+  const int rest = p.total - p.full;
+  p.split = rest ? std::min(units / rest, TN / CH) : 1;
+  if (p.full == 0) units = rest * p.split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2u * (unsigned)units);
   cfg.blockDim = dim3(NTHR);
@@ -486,7 +444,7 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, th, p);
+  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8");
 }
 
@@ -499,6 +457,7 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.w_rowsum = g.w_rowsum; p.bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
   p.T = (int)g.T; p.K = (int)g.K; p.N = (int)g.N; p.out_acc = g.out_acc;
   p.n_head = (int)g.n_head; p.out = g.out; p.head = g.head;
+  p.wide = (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");
   p.limit_ns = kWaitLimitNs;
