@@ -376,6 +376,14 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
 }
 
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
 // CTA pairs that are resident at once, per kernel and device (0 if the query fails).
 int resident_pairs(const void* kern, int smem, int threads) {
   static std::mutex mu;
@@ -448,6 +456,410 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8");
 }
 
+// ---- few tokens ------------------------------------------------------------------------------
+// Up to 8 tokens: bound by the weights' bytes (4096 x 4096: 16.8 MB, 2.6 us of HBM) and by latency, so
+// nothing is staged. A block takes 16 channels and all of K: its eight warps read the weight rows
+// straight into registers, all loads of a warp in flight together, and feed mma.sync (m16n8k32,
+// weights as the 16 rows, tokens as the 8 columns); their sums meet in shared memory.
+//
+// Operand layout: lane (g = lane / 4, i = lane % 4) reads 32 bytes, k = 128 s + 32 i ..., of the weight rows g
+// and g + 8 and of token g. An MMA adds products over its 32 k in any order, as long as both
+// operands have the same one, so each 8 bytes a lane holds serve as its share of one MMA: four
+// MMAs per 128 bytes, no shuffles, whole 128-byte lines from every row.
+constexpr int kRowTokens = 8;              // tokens at most: the MMA's columns
+constexpr int RT = 256;                    // threads
+constexpr int RW = RT / 32;
+
+struct Line { uint32_t v[8]; };
+
+// 32 bytes, zeros past the end of the row or of the rows
+__device__ __forceinline__ Line load32(const int8_t* p, bool in, bool wide) {
+  Line l;
+  if (!in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l.v[i] = 0u;
+  } else if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(l.v[0]), "=r"(l.v[1]), "=r"(l.v[2]), "=r"(l.v[3]), "=r"(l.v[4]),
+                   "=r"(l.v[5]), "=r"(l.v[6]), "=r"(l.v[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    l.v[0] = a.x; l.v[1] = a.y; l.v[2] = a.z; l.v[3] = a.w;
+    l.v[4] = b.x; l.v[5] = b.y; l.v[6] = b.z; l.v[7] = b.w;
+  }
+  return l;
+}
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct RowParams {
+  W8Params w;
+  bool wide_a, wide_w;     // the codes' bases are 32-byte aligned (their rows are: K % 32 == 0)
+};
+
+// what the epilogue needs of one output, read before the weights arrive
+struct OutConst { float alpha, mean, s, w1, b; };
+__device__ __forceinline__ OutConst out_const(const W8Params& p, int t, int o) {
+  OutConst c;
+  c.alpha = p.a_scale[t];
+  c.mean = p.mean ? p.mean[t] : 0.f;
+  c.s = p.w_scale[o];
+  c.w1 = p.mean ? p.w_rowsum[o] : 0.f;
+  c.b = p.bias ? __bfloat162float(p.bias[o]) : 0.f;
+  return c;
+}
+__device__ __forceinline__ void out_store(const W8Params& p, int t, int o, int sum,
+                                          const OutConst& c) {
+  if (p.out_acc) {
+    reinterpret_cast<int32_t*>(p.out)[(int64_t)t * p.N + o] = sum;
+    return;
+  }
+  const float y = __fmaf_rn((float)sum, __fmul_rn(c.alpha, c.s), __fmaf_rn(c.mean, c.w1, c.b));
+  if (o < p.n_head)
+    p.head[(int64_t)t * p.n_head + o] = y;
+  else
+    reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)t * p.N + o] = __float2bfloat16_rn(y);
+}
+
+// RU 128-byte segments of a warp in flight, blocks for RB to an SM
+template <int RU, int RB>
+__global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__ RowParams rp) {
+  const W8Params& p = rp.w;
+  __shared__ int s_part[RW][8][17];   // [warp][token][channel], one word of padding
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, i = lane & 3;
+  const int o0 = (int)blockIdx.x * 16;
+  const int segs = (p.K + 127) / 128;
+  const int8_t* w0 = p.w + (int64_t)(o0 + g) * p.K + 32 * i;
+  const int8_t* w1 = w0 + (int64_t)8 * p.K;
+  const int8_t* a0 = p.a + (int64_t)g * p.K + 32 * i;
+  const int et = tid >> 4, eo = o0 + (tid & 15);   // this thread's output
+  const bool out = et < p.T && tid < 128;
+  OutConst c = {};
+  if (out) c = out_const(p, et, eo);
+  int acc[4] = {};
+  for (int s0 = warp; s0 < segs; s0 += RW * RU) {
+    Line wr[RU][2], x[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const int k = (s0 + u * RW) * 128;
+      const bool in = k + 32 * i < p.K;   // N % 16 == 0: the channels are all there
+      wr[u][0] = load32(w0 + k, in, rp.wide_w);
+      wr[u][1] = load32(w1 + k, in, rp.wide_w);
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const int k = (s0 + u * RW) * 128;
+      x[u] = load32(a0 + k, k + 32 * i < p.K && g < p.T, rp.wide_a);
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        mma_s8(acc, wr[u][0].v[j], wr[u][1].v[j], wr[u][0].v[j + 1], wr[u][1].v[j + 1],
+               x[u].v[j], x[u].v[j + 1]);
+  }
+  // channels g and g + 8 of tokens 2 i and 2 i + 1
+  s_part[warp][2 * i][g] = acc[0];
+  s_part[warp][2 * i + 1][g] = acc[1];
+  s_part[warp][2 * i][g + 8] = acc[2];
+  s_part[warp][2 * i + 1][g + 8] = acc[3];
+  __syncthreads();
+  if (!out) return;
+  int sum = 0;
+#pragma unroll
+  for (int q = 0; q < RW; ++q) sum += s_part[q][et][tid & 15];
+  out_store(p, et, eo, sum, c);
+}
+
+oq_status run_rows(const W8Params& w, cudaStream_t s) {
+  RowParams p;
+  p.w = w;
+  p.wide_a = (reinterpret_cast<uintptr_t>(w.a) & 31u) == 0;
+  p.wide_w = (reinterpret_cast<uintptr_t>(w.w) & 31u) == 0;
+  // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
+  // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
+  // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
+  // (8 tokens) 4.6 against 6.0.
+  const unsigned grid = (unsigned)(w.N / 16);
+  if (w.K >= 4096 && grid <= 2u * 2u * (unsigned)sm_count())
+    k_gemm_w8_rows<4, 2><<<grid, RT, 0, s>>>(p);
+  else
+    k_gemm_w8_rows<2, 3><<<grid, RT, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_rows");
+}
+
+// ---- a few dozen to a few hundred tokens -----------------------------------------------------
+// Up to 256 tokens the weights' bytes still bound the product, and a tile for every 256 channels leaves
+// most SMs idle, so K is split too: a cluster of S CTAs owns 128 channels, CTA r its K blocks
+// [r ks, (r + 1) ks). All tokens at once: channels are the MMA's 128 rows (cta_group::1), tokens
+// its columns. Weights and tokens stream through a ring of TMA stages, weights by one thread and
+// tokens by another; the int32 partial sums go from TMEM to shared memory, and after a cluster
+// barrier CTA r adds its share of the tokens from all S CTAs through distributed shared memory.
+// Whole numbers add exactly in any order, so the result is that of the other shapes bit for bit.
+constexpr int PT = 256;                    // threads
+constexpr int PM = 128;                    // channels of a cluster
+constexpr int PWB = PM * 128;              // weight bytes of a K block
+constexpr int kSplitTokens = 256;          // tokens at most
+constexpr int kSplitMax = 8;               // CTAs of a cluster at most (portable size)
+constexpr int kRingMax = 12;               // stages at most
+
+struct SplitParams {
+  W8Params w;
+  int npad;                                // tokens, rounded up to 16 (the MMA's N)
+  int tcols;                               // TMEM columns: a power of two >= 32
+  int ks, nkb, ns;                         // K blocks of a CTA, in all; stages
+  int off_bar;                             // ring and partial sums lie in front of the barriers
+};
+
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(PT)
+    k_gemm_w8_split(const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_a,
+                    const __grid_constant__ SplitParams sp) {
+  const W8Params& p = sp.w;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.off_bar);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kRingMax + 1);   // TMEM base, abort
+  volatile uint32_t* s_abort = misc + 1;
+  float2* s_tok = reinterpret_cast<float2*>(smem + sp.off_bar + 256);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = (int)dev::cluster_nctarank(), r = (int)dev::cluster_ctarank();
+  const int o0 = ((int)blockIdx.x / S) * PM;
+  const int kb0 = r * sp.ks, nk = max(0, min(sp.nkb, kb0 + sp.ks) - kb0);
+  const int ns = sp.ns, xb = sp.npad * 128, stage = PWB + xb;
+  auto full = [&](int st) { return dev::smem_u32(&bars[st]); };
+  auto free_bar = [&](int st) { return dev::smem_u32(&bars[kRingMax + st]); };
+  const uint32_t done = dev::smem_u32(&bars[2 * kRingMax]);
+
+  if (tid == 0) {
+    for (int st = 0; st < ns; ++st) {
+      dev::mbar_init(full(st), 2);
+      dev::mbar_init(free_bar(st), 1);
+    }
+    dev::mbar_init(done, 1);
+    misc[1] = 0u;
+    dev::fence_mbar_init();
+    dev::prefetch_tmap(&tm_w);
+    dev::prefetch_tmap(&tm_a);
+  }
+  if (warp == 1) {
+    dev::tmem_alloc(dev::smem_u32(&misc[0]), (uint32_t)sp.tcols);
+    dev::tmem_relinquish();
+  }
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  int issued = 0;   // stages this thread filled (the producers)
+  if (warp == 0 || warp == 2) {
+    // ---------------- producers: warp 0 the weights, warp 2 the tokens ----------------
+    if (warp == 2) dependency_wait();   // the weights do not come from the launch before
+    if (lane == 0) {
+      for (int k = 0; k < nk; ++k) {
+        const int st = k % ns;
+        if (k >= ns && (!dev::mbar_wait(free_bar(st), (uint32_t)((k / ns) - 1) & 1u, p.err,
+                                        kSiteGemmEmpty, p.limit_ns) || *s_abort)) {
+          *s_abort = 1u;
+          break;
+        }
+        uint8_t* dst = smem + st * stage;
+        if (warp == 0) {
+          dev::mbar_arrive_expect_tx(full(st), (uint32_t)PWB);
+          dev::tma_load_2d(dev::smem_u32(dst), &tm_w, (kb0 + k) * 128, o0, full(st));
+        } else {
+          dev::mbar_arrive_expect_tx(full(st), (uint32_t)xb);
+          dev::tma_load_2d(dev::smem_u32(dst + PWB), &tm_a, (kb0 + k) * 128, 0, full(st));
+        }
+        issued = k + 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && lane == 0) {
+    // ---------------- MMA issuer ----------------
+    const uint32_t idesc = dev::idesc_i8(PM, sp.npad);
+    for (int k = 0; k < nk; ++k) {
+      const int st = k % ns;
+      if (!dev::mbar_wait(full(st), (uint32_t)(k / ns) & 1u, p.err, kSiteGemmFull, p.limit_ns)) {
+        *s_abort = 1u;
+        break;
+      }
+      dev::tc_fence_after();
+      const uint32_t sw = dev::smem_u32(smem + st * stage), sx = sw + PWB;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        dev::mma_i8(tmem, dev::sdesc_sw128(sw + kk * 32), dev::sdesc_sw128(sx + kk * 32), idesc,
+                    (k | kk) != 0);
+      dev::mma_commit(free_bar(st));
+    }
+    dev::mma_commit(done);   // arrives once every MMA issued above has completed
+  }
+  if (warp != 2) dependency_wait();
+
+  // this CTA's share of the tokens, their scales and means; this lane's four channels
+  const int per = (p.T + S - 1) / S, t0 = min(p.T, r * per), t1 = min(p.T, t0 + per);
+  for (int t = t0 + tid; t < t1; t += PT)
+    s_tok[t - t0] = make_float2(p.a_scale[t], p.mean ? p.mean[t] : 0.f);
+  const int o = o0 + lane * 4;
+  const bool has = o < p.N;   // N % 16 == 0: the four channels lie all inside or all outside
+  float2 cs[2], cw[2], cb[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    cs[i] = has ? make_float2(p.w_scale[o + 2 * i], p.w_scale[o + 2 * i + 1]) : make_float2(0.f, 0.f);
+    cw[i] = has && p.mean ? make_float2(p.w_rowsum[o + 2 * i], p.w_rowsum[o + 2 * i + 1])
+                          : make_float2(0.f, 0.f);
+    cb[i] = has && p.bias ? make_float2(__bfloat162float(p.bias[o + 2 * i]),
+                                        __bfloat162float(p.bias[o + 2 * i + 1]))
+                          : make_float2(0.f, 0.f);
+  }
+
+  // ---- partial sums: TMEM -> shared memory, int32 [token][128 channels] ----
+  {
+    bool ok = true;
+    if (lane == 0) ok = dev::mbar_wait(done, 0, p.err, kSiteGemmAccum, p.limit_ns);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0 && nk > 0 && *s_abort == 0u;
+    dev::tc_fence_after();
+    int32_t* part = reinterpret_cast<int32_t*>(smem);   // the stages are consumed
+    const int q = warp & 3;
+    for (int c = warp >> 2; c < sp.npad / 16; c += 2) {
+      uint32_t v[16];
+      dev::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * 16), v);
+      dev::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(c * 16 + j) * PM + q * 32 + lane] = ok ? (int32_t)v[j] : 0;
+    }
+  }
+  dev::tc_fence_before();
+  __syncwarp();
+  dev::cluster_sync();   // every CTA's partial sums and token scales are in place
+
+  // ---- sum over the cluster and epilogue: a warp takes a token's 128 channels ----
+  {
+    const uint32_t mine = dev::smem_u32(smem) + (uint32_t)lane * 16u;
+    constexpr int TU = 2;   // tokens of a warp whose remote loads are in flight together
+    for (int tb = t0 + warp; tb < t1; tb += TU * (PT / 32)) {
+      int4 sum[TU];
+#pragma unroll
+      for (int u = 0; u < TU; ++u) sum[u] = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int sr = 0; sr < kSplitMax; ++sr) {
+        if (sr >= S) break;
+        const uint32_t peer = dev::map_to_cta(mine, (uint32_t)sr);
+#pragma unroll
+        for (int u = 0; u < TU; ++u) {
+          const int t = tb + u * (PT / 32);
+          if (t < t1) {
+            const uint4 v = dev::ld_cluster_v4(peer + (uint32_t)t * (PM * 4));
+            sum[u].x += (int)v.x; sum[u].y += (int)v.y;
+            sum[u].z += (int)v.z; sum[u].w += (int)v.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
+        const int t = tb + u * (PT / 32);
+        if (t >= t1 || !has) continue;
+        if (p.out_acc) {
+          *reinterpret_cast<int4*>(reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o) = sum[u];
+          continue;
+        }
+        const float2 tk = s_tok[t - t0];
+        const float2 al = make_float2(tk.x, tk.x), mn = make_float2(tk.y, tk.y);
+        const float2 y0 = __ffma2_rn(make_float2((float)sum[u].x, (float)sum[u].y),
+                                     __fmul2_rn(al, cs[0]), __ffma2_rn(mn, cw[0], cb[0]));
+        const float2 y1 = __ffma2_rn(make_float2((float)sum[u].z, (float)sum[u].w),
+                                     __fmul2_rn(al, cs[1]), __ffma2_rn(mn, cw[1], cb[1]));
+        if (o < p.n_head)
+          *reinterpret_cast<float4*>(p.head + (int64_t)t * p.n_head + o) =
+              make_float4(y0.x, y0.y, y1.x, y1.y);
+        else
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t * p.N + o) =
+              make_uint2(pack2(y0), pack2(y1));
+      }
+    }
+  }
+  __syncwarp();
+  dev::cluster_sync();   // no CTA leaves while another still reads its partial sums
+
+  // after an abort, loads already issued may still land: wait for them (bounded)
+  if (lane == 0 && (warp == 0 || warp == 2) && *s_abort != 0u)
+    for (int k = max(0, issued - ns); k < issued; ++k)
+      dev::mbar_wait(full(k % ns), (uint32_t)(k / ns) & 1u, p.err, kSiteGemmDrain, p.limit_ns);
+  __syncwarp();
+  if (warp == 1) {
+    dev::tc_fence_after();
+    dev::tmem_dealloc(tmem, (uint32_t)sp.tcols);
+  }
+}
+
+oq_status run_split(const W8Params& w, cudaStream_t s) {
+  SplitParams p{};
+  p.w = w;
+  p.npad = (w.T + 15) / 16 * 16;
+  p.tcols = 32;
+  while (p.tcols < p.npad) p.tcols *= 2;
+  p.nkb = (w.K + 127) / 128;
+  const int tiles = (w.N + PM - 1) / PM, sms = sm_count();
+  // The split that leaves the fullest SM the fewest K blocks; of equal ones the smallest. A further
+  // CTA in the cluster costs about as much as a sixteenth of a K block's time in barriers.
+  int best = 1, ks = p.nkb;
+  int64_t cost = INT64_MAX;
+  for (int S = 1; S <= kSplitMax; ++S) {
+    const int k = (p.nkb + S - 1) / S;
+    if ((S - 1) * k >= p.nkb) continue;   // a CTA would have nothing to do
+    const int64_t c = 16 * (((int64_t)tiles * S + sms - 1) / sms) * k + S;
+    if (c < cost) cost = c, best = S, ks = k;
+  }
+  p.ks = ks;
+  // ring: as deep as the CTA has blocks, within half an SM's shared memory where the tokens are few
+  // (two CTAs to an SM), else within all of it; at least as large as the partial sums
+  const int stage = PWB + p.npad * 128;
+  const int room = p.npad <= 64 ? 108 * 1024 : 216 * 1024;
+  p.ns = std::min(std::min(ks, kRingMax), room / stage);
+  const int ring = std::max(p.ns * stage, p.npad * PM * 4);
+  p.off_bar = (ring + 1023) / 1024 * 1024;
+  const int smem = p.off_bar + 256 + 8 * kSplitTokens + 1024;
+  CUtensorMap tw, ta;
+  const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
+  if (!tma_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, PM,
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tma_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.a, K, T, K, 128, (uint32_t)p.npad,
+                  CU_TENSOR_MAP_SWIZZLE_128B))
+    return fail(OQ_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable");
+  const auto kern = &k_gemm_w8_split;
+  cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8_split)");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * best));
+  cfg.blockDim = dim3(PT);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)best;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tw, ta, p);
+  return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_split");
+}
+
 }  // namespace
 
 oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
@@ -461,6 +873,8 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");
   p.limit_ns = kWaitLimitNs;
+  if (g.T <= kRowTokens) return run_rows(p, s);
+  if (g.T <= kSplitTokens) return run_split(p, s);
   return run_tiles(p, s);
 }
 
