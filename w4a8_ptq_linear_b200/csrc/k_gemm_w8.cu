@@ -41,6 +41,29 @@ struct W8Params {
   unsigned long long limit_ns;
 };
 
+// A walk over the stages of a ring. One thread issues a role's steps, so its own instructions are on
+// the critical path: a division for the stage and the phase of each step took 0.1 us of it.
+struct Ring {
+  int st = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++st == n) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Wait for a stage's barrier; false (and the CTA's abort flag set) when the wait gave up or another
+// role has. The flag is looked at only where the stage was not ready.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
+                                          const W8Params& p, uint32_t site) {
+  if (dev::mbar_try_wait(bar, parity)) return true;
+  if (*abort == 0u && dev::mbar_wait(bar, parity, p.err, site, p.limit_ns)) return true;
+  *abort = 1u;
+  return false;
+}
+
 // ---- tiles on CTA pairs ----------------------------------------------------------------------
 // D[t, o] on tcgen05 (kind::i8, cta_group::2): 256 tokens are the M rows, up to 256 channels the
 // N columns, so that a thread of the epilogue holds one token's row of the accumulator: its scale
@@ -214,17 +237,16 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (lane == 0) {
       const bool tok = warp == 0;
       uint32_t j = 0;
+      Ring rg;
       bool ok = true;
       while (ok && it.next(m, c0, nch)) {
         const int rows = nch * CH / 2;                      // this CTA's weight rows
         const int boxes = tok ? 1 : (rows + BBOX - 1) / BBOX;
         const uint32_t block_bytes = tok ? 2u * AK : 2u * boxes * BBOX * 128u;   // of both CTAs
         const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * CH + (int)rank * rows;
-        for (int st = 0; st < nst; ++st, ++j) {
-          const int s = j % SK, nk = min(KS, nkb - st * KS);
-          if (!dev::mbar_wait(free_bar(s), ((j / SK) & 1u) ^ 1u, p.err, kSiteGemmEmpty,
-                              p.limit_ns) || *s_abort) {
-            give_up();
+        for (int st = 0; st < nst; ++st, ++j, rg.next(SK)) {
+          const int s = rg.st, nk = min(KS, nkb - st * KS);
+          if (!ring_wait(free_bar(s), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) {
             ok = false;
             break;
           }
@@ -254,35 +276,34 @@ __global__ void __launch_bounds__(NTHR, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (the leader's lane 0) ----------------
     if (lane == 0 && rank == 0) {
-      uint32_t j = 0, n = 0;
+      const uint64_t da = dev::sdesc_sw128(dev::smem_u32(smem));
+      const uint64_t db = dev::sdesc_sw128(dev::smem_u32(smem) + OFF_B);
+      uint32_t n = 0;
+      Ring rg;
       bool ok = true, issued = false;
       for (; ok && it.next(m, c0, nch); ++n) {
         const uint32_t idesc = dev::idesc_i8(2 * TM, nch * CH);
         const int b = n & 1;
-        if (!dev::mbar_wait(tempty_bar(b), ((n >> 1) & 1u) ^ 1u, p.err, kSiteGemmAccum,
-                            p.limit_ns) || *s_abort) {
-          give_up();
+        if (!ring_wait(tempty_bar(b), ((n >> 1) & 1u) ^ 1u, s_abort, p, kSiteGemmAccum)) {
           ok = false;
           break;
         }
         dev::tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)(b * TN);
-        for (int st = 0; st < nst; ++st, ++j) {
-          const int s = j % SK, nk = min(KS, nkb - st * KS);
-          if (!dev::mbar_wait(full_bar(s), (j / SK) & 1u, p.err, kSiteGemmFull, p.limit_ns)) {
-            give_up();
+        for (int st = 0; st < nst; ++st, rg.next(SK)) {
+          const int s = rg.st, nk = min(KS, nkb - st * KS);
+          if (!ring_wait(full_bar(s), rg.phase, s_abort, p, kSiteGemmFull)) {
             ok = false;
             break;
           }
           dev::tc_fence_after();
-          const uint32_t sa = dev::smem_u32(smem + s * AB), sb = dev::smem_u32(smem + OFF_B + s * BB);
+          const uint64_t sa = da + (uint64_t)(s * AB >> 4), sb = db + (uint64_t)(s * BB >> 4);
 #pragma unroll
           for (int u = 0; u < KS; ++u) {
             if (u >= nk) break;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              dev::mma_i8_pair(dt, dev::sdesc_sw128(sa + u * AK + kk * 32),
-                               dev::sdesc_sw128(sb + u * BK + kk * 32), idesc,
+              dev::mma_i8_pair(dt, sa + (u * AK >> 4) + 2 * kk, sb + (u * BK >> 4) + 2 * kk, idesc,
                                (st | u | kk) != 0);
           }
           issued = true;
@@ -672,21 +693,15 @@ __global__ void __launch_bounds__(PT)
     // ---------------- producers: warp 0 the weights, warp 2 the tokens ----------------
     if (warp == 2) dependency_wait();   // the weights do not come from the launch before
     if (lane == 0) {
-      for (int k = 0; k < nk; ++k) {
-        const int st = k % ns;
-        if (k >= ns && (!dev::mbar_wait(free_bar(st), (uint32_t)((k / ns) - 1) & 1u, p.err,
-                                        kSiteGemmEmpty, p.limit_ns) || *s_abort)) {
-          *s_abort = 1u;
-          break;
-        }
-        uint8_t* dst = smem + st * stage;
-        if (warp == 0) {
-          dev::mbar_arrive_expect_tx(full(st), (uint32_t)PWB);
-          dev::tma_load_2d(dev::smem_u32(dst), &tm_w, (kb0 + k) * 128, o0, full(st));
-        } else {
-          dev::mbar_arrive_expect_tx(full(st), (uint32_t)xb);
-          dev::tma_load_2d(dev::smem_u32(dst + PWB), &tm_a, (kb0 + k) * 128, 0, full(st));
-        }
+      const uint32_t first = dev::smem_u32(smem) + (warp == 0 ? 0u : (uint32_t)PWB);
+      const uint32_t bytes = warp == 0 ? (uint32_t)PWB : (uint32_t)xb;
+      const CUtensorMap* map = warp == 0 ? &tm_w : &tm_a;
+      const int row = warp == 0 ? o0 : 0;
+      Ring rg;
+      for (int k = 0; k < nk; ++k, rg.next(ns)) {
+        if (k >= ns && !ring_wait(free_bar(rg.st), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) break;
+        dev::mbar_arrive_expect_tx(full(rg.st), bytes);
+        dev::tma_load_2d(first + (uint32_t)(rg.st * stage), map, (kb0 + k) * 128, row, full(rg.st));
         issued = k + 1;
       }
     }
@@ -694,19 +709,17 @@ __global__ void __launch_bounds__(PT)
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer ----------------
     const uint32_t idesc = dev::idesc_i8(PM, sp.npad);
-    for (int k = 0; k < nk; ++k) {
-      const int st = k % ns;
-      if (!dev::mbar_wait(full(st), (uint32_t)(k / ns) & 1u, p.err, kSiteGemmFull, p.limit_ns)) {
-        *s_abort = 1u;
-        break;
-      }
+    const uint64_t dw = dev::sdesc_sw128(dev::smem_u32(smem));
+    const uint64_t dx = dev::sdesc_sw128(dev::smem_u32(smem) + PWB);
+    Ring rg;
+    for (int k = 0; k < nk; ++k, rg.next(ns)) {
+      if (!ring_wait(full(rg.st), rg.phase, s_abort, p, kSiteGemmFull)) break;
       dev::tc_fence_after();
-      const uint32_t sw = dev::smem_u32(smem + st * stage), sx = sw + PWB;
+      const uint64_t at = (uint64_t)((uint32_t)(rg.st * stage) >> 4);   // of the stage, 16-byte units
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        dev::mma_i8(tmem, dev::sdesc_sw128(sw + kk * 32), dev::sdesc_sw128(sx + kk * 32), idesc,
-                    (k | kk) != 0);
-      dev::mma_commit(free_bar(st));
+        dev::mma_i8(tmem, dw + at + 2 * kk, dx + at + 2 * kk, idesc, (k | kk) != 0);
+      dev::mma_commit(free_bar(rg.st));
     }
     dev::mma_commit(done);   // arrives once every MMA issued above has completed
   }
