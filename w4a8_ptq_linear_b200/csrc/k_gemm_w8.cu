@@ -478,7 +478,7 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
 }
 
 // ---- few tokens ------------------------------------------------------------------------------
-// Up to 8 tokens: bound by the weights' bytes (4096 x 4096: 16.8 MB, 2.6 us of HBM) and by latency, so
+// Up to 32 tokens: bound by the weights' bytes (4096 x 4096: 16.8 MB, 2.6 us of HBM) and by latency, so
 // nothing is staged. A block takes 16 channels and all of K: its eight warps read the weight rows
 // straight into registers, all loads of a warp in flight together, and feed mma.sync (m16n8k32,
 // weights as the 16 rows, tokens as the 8 columns); their sums meet in shared memory.
@@ -487,7 +487,7 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
 // and g + 8 and of token g. An MMA adds products over its 32 k in any order, as long as both
 // operands have the same one, so each 8 bytes a lane holds serve as its share of one MMA: four
 // MMAs per 128 bytes, no shuffles, whole 128-byte lines from every row.
-constexpr int kRowTokens = 8;              // tokens at most: the MMA's columns
+constexpr int kRowTokens = 32;             // tokens at most: four groups of the MMA's columns
 constexpr int RT = 256;                    // threads
 constexpr int RW = RT / 32;
 
@@ -551,11 +551,11 @@ __device__ __forceinline__ void out_store(const W8Params& p, int t, int o, int s
     reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)t * p.N + o] = __float2bfloat16_rn(y);
 }
 
-// RU 128-byte segments of a warp in flight, blocks for RB to an SM
-template <int RU, int RB>
+// NT groups of eight tokens; RU 128-byte segments of a warp in flight; blocks for RB to an SM
+template <int NT, int RU, int RB>
 __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__ RowParams rp) {
   const W8Params& p = rp.w;
-  __shared__ int s_part[RW][8][17];   // [warp][token][channel], one word of padding
+  __shared__ int s_part[RW][NT * 8][17];   // [warp][token][channel], one word of padding
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, i = lane & 3;
   const int o0 = (int)blockIdx.x * 16;
@@ -563,13 +563,15 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
   const int8_t* w0 = p.w + (int64_t)(o0 + g) * p.K + 32 * i;
   const int8_t* w1 = w0 + (int64_t)8 * p.K;
   const int8_t* a0 = p.a + (int64_t)g * p.K + 32 * i;
-  const int et = tid >> 4, eo = o0 + (tid & 15);   // this thread's output
-  const bool out = et < p.T && tid < 128;
-  OutConst c = {};
-  if (out) c = out_const(p, et, eo);
-  int acc[4] = {};
+  // this thread's outputs: channel tid % 16 of tokens tid / 16, tid / 16 + 16; their constants are
+  // read ahead where there are registers for them
+  constexpr int NO = NT > 2 ? 2 : 1;
+  const int oc = tid & 15;
+  OutConst c0 = {};
+  if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
+  int acc[NT][4] = {};
   for (int s0 = warp; s0 < segs; s0 += RW * RU) {
-    Line wr[RU][2], x[RU];
+    Line wr[RU][2], x[RU][NT];
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       const int k = (s0 + u * RW) * 128;
@@ -580,26 +582,53 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       const int k = (s0 + u * RW) * 128;
-      x[u] = load32(a0 + k, k + 32 * i < p.K && g < p.T, rp.wide_a);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        x[u][n] = load32(a0 + (int64_t)(n * 8) * p.K + k, k + 32 * i < p.K && n * 8 + g < p.T,
+                         rp.wide_a);
     }
 #pragma unroll
     for (int u = 0; u < RU; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; j += 2)
-        mma_s8(acc, wr[u][0].v[j], wr[u][1].v[j], wr[u][0].v[j + 1], wr[u][1].v[j + 1],
-               x[u].v[j], x[u].v[j + 1]);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          mma_s8(acc[n], wr[u][0].v[j], wr[u][1].v[j], wr[u][0].v[j + 1], wr[u][1].v[j + 1],
+                 x[u][n].v[j], x[u][n].v[j + 1]);
   }
   // channels g and g + 8 of tokens 2 i and 2 i + 1
-  s_part[warp][2 * i][g] = acc[0];
-  s_part[warp][2 * i + 1][g] = acc[1];
-  s_part[warp][2 * i][g + 8] = acc[2];
-  s_part[warp][2 * i + 1][g + 8] = acc[3];
-  __syncthreads();
-  if (!out) return;
-  int sum = 0;
 #pragma unroll
-  for (int q = 0; q < RW; ++q) sum += s_part[q][et][tid & 15];
-  out_store(p, et, eo, sum, c);
+  for (int n = 0; n < NT; ++n) {
+    s_part[warp][n * 8 + 2 * i][g] = acc[n][0];
+    s_part[warp][n * 8 + 2 * i + 1][g] = acc[n][1];
+    s_part[warp][n * 8 + 2 * i][g + 8] = acc[n][2];
+    s_part[warp][n * 8 + 2 * i + 1][g + 8] = acc[n][3];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < NO; ++e) {
+    const int t = (tid >> 4) + 16 * e;
+    if (t >= p.T) break;   // T <= 8 NT
+    int sum = 0;
+#pragma unroll
+    for (int q = 0; q < RW; ++q) sum += s_part[q][t][oc];
+    out_store(p, t, o0 + oc, sum, NO == 1 ? c0 : out_const(p, t, o0 + oc));
+  }
+}
+
+template <int NT>
+void launch_rows(const RowParams& p, cudaStream_t s) {
+  // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
+  // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
+  // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
+  // (8 tokens) 4.6 against 6.0. 16 tokens: 4096 x 4096 6.6 against 6.9; the other way
+  // 4096 x 12288 13.7 against 14.6, 1920 x 5760 (24 tokens) 6.4 against 8.0.
+  const unsigned grid = (unsigned)(p.w.N / 16);
+  constexpr int D = NT == 1 ? 2 : 1;
+  if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)sm_count())
+    k_gemm_w8_rows<NT, 2 * D, 2><<<grid, RT, 0, s>>>(p);
+  else
+    k_gemm_w8_rows<NT, D, 3><<<grid, RT, 0, s>>>(p);
 }
 
 oq_status run_rows(const W8Params& w, cudaStream_t s) {
@@ -607,15 +636,10 @@ oq_status run_rows(const W8Params& w, cudaStream_t s) {
   p.w = w;
   p.wide_a = (reinterpret_cast<uintptr_t>(w.a) & 31u) == 0;
   p.wide_w = (reinterpret_cast<uintptr_t>(w.w) & 31u) == 0;
-  // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
-  // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
-  // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
-  // (8 tokens) 4.6 against 6.0.
-  const unsigned grid = (unsigned)(w.N / 16);
-  if (w.K >= 4096 && grid <= 2u * 2u * (unsigned)sm_count())
-    k_gemm_w8_rows<4, 2><<<grid, RT, 0, s>>>(p);
-  else
-    k_gemm_w8_rows<2, 3><<<grid, RT, 0, s>>>(p);
+  if (w.T <= 8) launch_rows<1>(p, s);
+  else if (w.T <= 16) launch_rows<2>(p, s);
+  else if (w.T <= 24) launch_rows<3>(p, s);
+  else launch_rows<4>(p, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_rows");
 }
