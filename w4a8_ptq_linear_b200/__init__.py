@@ -460,76 +460,88 @@ def linear_static_scratch(plan: Plan, x, w_packed, w_scale, w_rowsum=None, bias=
 
 
 # ---- INT8 weights and the attention input -----------------------------------------------------
+# These calls cost a few microseconds on the GPU where tokens are few, so their checks are one
+# comparison to a property; what is wrong is worked out in _refuse.
 
-def _need(t, name, dtype, ndim=None):
-    """The tensor's device pointer, or OQError where the library could not read it: another
-    type, on the host or another device, rows that are not contiguous."""
+def _refuse(t, name, dtype, shape=None):
+    """OQError for a tensor the library could not read: another type or size, on the host or
+    another device, elements that do not follow one another."""
     import torch
-    if t.dtype != dtype or (ndim is not None and t.dim() != ndim):
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a {ndim}-d {dtype} tensor, got "
-                                          f"{t.dim()}-d {t.dtype}")
+    what = f"{name}: {t.dtype} {tuple(t.shape)}"
+    if t.dtype != dtype:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        want = f"{shape[0]} elements" if len(shape) == 1 else tuple(shape)
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what}, expected {want}")
     if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
-    if not t.is_contiguous():
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: must be contiguous")
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} on {t.device}, not the current CUDA device")
+    raise OQError(OQ_ERR_INVALID_ARG, f"{what}: must be contiguous, strides {t.stride()}")
+
+
+def _device():
+    """Index of the current CUDA device; -2, where no tensor is, before CUDA is in use."""
+    import torch
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _raw_stream(stream, dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _need(t, name, dtype, shape, dev):
+    """The device pointer of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
     return t.data_ptr()
 
 
-def _need_vec(t, name, dtype, n):
-    """As _need for an optional vector of n elements (None: NULL)."""
-    if t is None:
-        return None
-    p = _need(t, name, dtype, 1)
-    if t.shape[0] != n:
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {t.shape[0]} elements, expected {n}")
-    return p
+def _need_opt(t, name, dtype, shape, dev):
+    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
-def _need_rows(t, name, d):
-    """Pointer and pitch of a bf16 [T, d] tensor whose rows may lie apart."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != d or (
-            t.shape[1] > 1 and t.stride(1) != 1):
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a bfloat16 [T, {d}] tensor with "
-                                          "contiguous rows")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else d)
+def _need_rows(t, name, dtype, d, dev):
+    """Pointer and row pitch of a [rows, d] tensor whose rows may lie apart."""
+    if t.dim() != 2 or t.shape[1] != d:
+        _refuse(t, name, dtype, ("rows", d))
+    n, _ = t.shape
+    pitch, step = t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or step != 1:
+        _refuse(t, name, dtype)
+    return t.data_ptr(), n, pitch if n > 1 else d
 
 
-def _need_out(out, shape, dtype, dev, name="out"):
-    import torch
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(out, name, dtype, len(shape))
-    if tuple(out.shape) != tuple(shape):
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {tuple(out.shape)}, expected {tuple(shape)}")
-    return out
+def _need_2d(t, name, dtype, dev):
+    """Pointer and shape of a contiguous matrix."""
+    if t.dim() != 2 or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, None if t.dim() == 2 else ("rows", "columns"))
+    return t.data_ptr(), *t.shape
 
 
-def _scratch(workspace, need, dev, stream):
-    """The caller's workspace, or one from torch's allocator that stays in use on `stream`."""
+def _scratch(workspace, need, like, stream):
+    """Pointer and size of the caller's workspace, or of one from torch's allocator that stays
+    in use on `stream`; the tensor itself, to be kept until the call has been made."""
     import torch
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = like.new_empty(max(need, 256), dtype=torch.uint8)
         if stream is not None:
             workspace.record_stream(stream)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise OQError(OQ_ERR_INVALID_ARG, "workspace: must be a contiguous CUDA tensor")
-    return workspace, workspace.numel() * workspace.element_size()
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise OQError(OQ_ERR_INVALID_ARG, "workspace: must be contiguous, on the input's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def prepare_weights_w8(plan: Plan, w, *, stream=None):
     """oq_prepare_weights_w8 on a bf16 [n_out, d] CUDA tensor: (w_codes int8 [n_out, d],
     w_scale float32 [n_out], w_rowsum float32 [n_out])."""
     import torch
-    wp, ldw = _need_rows(w, "w", plan.d)
-    n = w.shape[0]
+    dev = _device()
+    wp, n, ldw = _need_rows(w, "w", torch.bfloat16, plan.d, dev)
     codes = torch.empty((n, plan.d), dtype=torch.int8, device=w.device)
     ws = torch.empty(n, dtype=torch.float32, device=w.device)
     w1 = torch.empty(n, dtype=torch.float32, device=w.device)
     _check(lib().oq_prepare_weights_w8(plan.handle, wp, n, ldw, codes.data_ptr(), ws.data_ptr(),
-                                       w1.data_ptr(), _stream(stream)))
+                                       w1.data_ptr(), _raw_stream(stream, dev)))
     return codes, ws, w1
 
 
@@ -537,17 +549,19 @@ def gemm_w8a8(a, a_scale, w_codes, w_scale, *, mean=None, w_rowsum=None, bias=No
               out_kind=OUT_BF16, out=None, stream=None):
     """oq_gemm_w8a8: int8 [T, K] codes x int8 [N, K] weights -> bf16 (or int32 sums) [T, N]."""
     import torch
-    f32 = torch.float32
-    ap, wp = _need(a, "a", torch.int8, 2), _need(w_codes, "w_codes", torch.int8, 2)
-    (T, K), N = a.shape, w_codes.shape[0]
-    if w_codes.shape[1] != K:
-        raise OQError(OQ_ERR_INVALID_ARG, f"a has {K} columns, w_codes {w_codes.shape[1]}")
-    out = _need_out(out, (T, N), torch.bfloat16 if out_kind == OUT_BF16 else torch.int32, a.device)
+    f32, dev = torch.float32, _device()
+    ap, T, K = _need_2d(a, "a", torch.int8, dev)
+    wp, N, Kw = _need_2d(w_codes, "w_codes", torch.int8, dev)
+    if Kw != K:
+        raise OQError(OQ_ERR_INVALID_ARG, f"a has {K} columns, w_codes {Kw}")
+    dt = torch.bfloat16 if out_kind == OUT_BF16 else torch.int32
+    if out is None:
+        out = a.new_empty((T, N), dtype=dt)
     _check(lib().oq_gemm_w8a8(
-        ap, _need_vec(a_scale, "a_scale", f32, T), _need_vec(mean, "mean", f32, T), wp,
-        _need_vec(w_scale, "w_scale", f32, N), _need_vec(w_rowsum, "w_rowsum", f32, N),
-        _need_vec(bias, "bias", torch.bfloat16, N), T, K, N, out_kind, out.data_ptr(),
-        _stream(stream)))
+        ap, _need(a_scale, "a_scale", f32, (T,), dev), _need_opt(mean, "mean", f32, (T,), dev), wp,
+        _need(w_scale, "w_scale", f32, (N,), dev), _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev),
+        _need_opt(bias, "bias", torch.bfloat16, (N,), dev), T, K, N, out_kind,
+        _need(out, "out", dt, (T, N), dev), _raw_stream(stream, dev)))
     return out
 
 
@@ -555,18 +569,18 @@ def linear_w8a8(plan: Plan, x, w_codes, w_scale, w_rowsum=None, bias=None, *, wo
                 out=None, stream=None):
     """oq_linear_w8a8: the whole layer against INT8 weights, bf16 [T, d] -> bf16 [T, N]."""
     import torch
-    f32 = torch.float32
-    xp, ldx = _need_rows(x, "x", plan.d)
-    wp = _need(w_codes, "w_codes", torch.int8, 2)
-    T, N = x.shape[0], w_codes.shape[0]
-    if w_codes.shape[1] != plan.d:
-        raise OQError(OQ_ERR_INVALID_ARG, f"w_codes: {w_codes.shape[1]} columns, plan d={plan.d}")
-    out = _need_out(out, (T, N), torch.bfloat16, x.device)
-    workspace, nbytes = _scratch(workspace, plan.workspace_bytes(T), x.device, stream)
+    f32, bf16, dev = torch.float32, torch.bfloat16, _device()
+    xp, T, ldx = _need_rows(x, "x", bf16, plan.d, dev)
+    wp, N, Kw = _need_2d(w_codes, "w_codes", torch.int8, dev)
+    if Kw != plan.d:
+        raise OQError(OQ_ERR_INVALID_ARG, f"w_codes: {Kw} columns, plan d={plan.d}")
+    if out is None:
+        out = x.new_empty((T, N))
+    ws, nbytes, keep = _scratch(workspace, plan.workspace_bytes(T), x, stream)
     _check(lib().oq_linear_w8a8(
-        plan.handle, xp, T, ldx, wp, _need_vec(w_scale, "w_scale", f32, N),
-        _need_vec(w_rowsum, "w_rowsum", f32, N), _need_vec(bias, "bias", torch.bfloat16, N), N,
-        out.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+        plan.handle, xp, T, ldx, wp, _need(w_scale, "w_scale", f32, (N,), dev),
+        _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev), _need_opt(bias, "bias", bf16, (N,), dev),
+        N, _need(out, "out", bf16, (T, N), dev), ws, nbytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -582,63 +596,56 @@ class Heads:
     """The query and key heads of an attention input (oq_heads): their norm ("none", "rms",
     "layer") with float32 [head_dim] weights and biases, and their rotation ("none", "pairs",
     "halves") with float32 [n_pos, rot_dim / 2] tables of cosines and sines. It keeps the
-    tensors alive and can be used by any number of calls."""
+    tensors alive and can be used by any number of calls on the device it was made on."""
 
     def __init__(self, head_dim, q_heads, k_heads, *, norm="rms", eps=1e-6, q_weight=None,
                  q_bias=None, k_weight=None, k_bias=None, rope="none", cos=None, sin=None):
         import torch
-        f32 = torch.float32
+        f32, dev = torch.float32, _device()
         if norm not in NORMS or rope not in ROPES:
             raise OQError(OQ_ERR_INVALID_ARG, f"unknown norm {norm!r} or rope {rope!r}")
         self.head_dim, self.q_heads, self.k_heads = head_dim, q_heads, k_heads
         self._keep = (q_weight, q_bias, k_weight, k_bias, cos, sin)
-        vec = [_need_vec(t, n, f32, head_dim) for t, n in
+        vec = [_need_opt(t, n, f32, (head_dim,), dev) for t, n in
                ((q_weight, "q_weight"), (q_bias, "q_bias"), (k_weight, "k_weight"),
                 (k_bias, "k_bias"))]
         tab, rot, n_pos = [None, None], 0, 0
         if rope != "none":
-            if cos is None or sin is None or cos.shape != sin.shape:
+            if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
                 raise OQError(OQ_ERR_INVALID_ARG, "cos and sin: two tables of the same shape")
-            tab = [_need(cos, "cos", f32, 2), _need(sin, "sin", f32, 2)]
+            tab = [_need(t, n, f32, cos.shape, dev) for t, n in ((cos, "cos"), (sin, "sin"))]
             n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        self.device = next((t.device for t in self._keep if t is not None), None)
+        self.device = dev if any(vec + tab) else None   # without tensors: any
         self._s = _HeadsStruct(head_dim, q_heads, k_heads, NORMS[norm], ROPES[rope], rot, eps,
                                *vec, *tab, n_pos)
         self._ref = ctypes.addressof(self._s)
+
+    def _check_device(self, dev):
+        if self.device not in (None, dev):
+            raise OQError(OQ_ERR_INVALID_ARG, f"heads belong to device {self.device}, current "
+                                              f"device is {dev}")
 
 
 _Strides = _I64 * 3
 
 
-def _head_rows(t, name, heads):
-    """(pointer, strides) of a bf16 [B, S, heads.., D] view whose elements are contiguous."""
+def _head_rows(t, name, dev):
+    """(pointer, strides) of a bf16 [S, heads, D] or [B, S, heads, D] view, elements contiguous."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() not in (3, 4) or t.stride(-1) != 1:
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: expected a bfloat16 [S, heads, head_dim] or "
-                                          "[B, S, heads, head_dim] tensor, elements contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise OQError(OQ_ERR_INVALID_ARG, f"{name}: on {t.device}, not the current CUDA device")
     st = t.stride()
-    return t.data_ptr(), _Strides(*(st[:3] if len(st) == 4 else (0, st[0], st[1])))
+    if len(st) not in (3, 4) or t.dtype is not torch.bfloat16 or t.get_device() != dev or st[-1] != 1:
+        _refuse(t, name, torch.bfloat16, None if len(st) in (3, 4) else ("[B,] S", "heads", "D"))
+    return t.data_ptr(), _Strides(*st[:3]) if len(st) == 4 else _Strides(0, st[0], st[1])
 
 
-def _positions(positions, B, S):
+def _positions(positions, B, S, dev):
     """(pointer, batch stride) of int32 [S] or [B, S] positions."""
     import torch
     if positions is None:
         return None, 0
-    if positions.dim() not in (1, 2) or tuple(positions.shape) not in ((S,), (B, S)):
-        raise OQError(OQ_ERR_INVALID_ARG, f"positions: {tuple(positions.shape)}, expected "
-                                          f"({S},) or ({B}, {S})")
-    return (_need(positions, "positions", torch.int32, positions.dim()),
-            S if positions.dim() == 2 else 0)
-
-
-def _check_heads_device(heads):
-    import torch
-    if heads.device is not None and heads.device.index != torch.cuda.current_device():
-        raise OQError(OQ_ERR_INVALID_ARG, f"heads: its tensors are on {heads.device}, not the "
-                                          "current CUDA device")
+    one = positions.dim() == 1
+    return (_need(positions, "positions", torch.int32, (S,) if one else (B, S), dev),
+            0 if one else S)
 
 
 def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, stream=None):
@@ -647,33 +654,43 @@ def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, 
     or [B, S], default 0..S-1; a negative one leaves its token unrotated. Returns (q_out, k_out),
     new contiguous tensors unless given; an output may be its input."""
     import torch
-    _check_heads_device(heads)
-    io, lead, dev = [], None, None
-    for t, o, name, n in ((q, q_out, "q", heads.q_heads), (k, k_out, "k", heads.k_heads)):
-        if t is None:
-            if n or o is not None:
-                raise OQError(OQ_ERR_INVALID_ARG, f"{name}: missing, with {n} heads")
-            io.append((None, None, None, None, None))
-            continue
-        shape = tuple(t.shape)
-        if shape[-2:] != (n, heads.head_dim) or (lead is not None and shape[:-2] != lead):
-            raise OQError(OQ_ERR_INVALID_ARG, f"{name}: {shape}, expected "
-                                              f"{lead or '[B,] S'} x ({n}, {heads.head_dim})")
-        lead, dev = shape[:-2], t.device
-        ip, ist = _head_rows(t, name, heads)
-        if o is None:
-            o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        elif tuple(o.shape) != shape:
-            raise OQError(OQ_ERR_INVALID_ARG, f"{name}_out: {tuple(o.shape)}, expected {shape}")
-        op, ost = _head_rows(o, name + "_out", heads)
-        io.append((ip, ist, op, ost, o))
+    dev = _device()
+    heads._check_device(dev)
+    lead = None
+    qp = qs = qop = qos = kp = ks = kop = kos = None
+    if q is not None:
+        shape = q.shape
+        lead = shape[:-2]
+        if shape != (*lead, heads.q_heads, heads.head_dim):
+            _refuse(q, "q", torch.bfloat16, ("[B,] S", heads.q_heads, heads.head_dim))
+        qp, qs = _head_rows(q, "q", dev)
+        if q_out is None:
+            q_out = q.new_empty(shape)
+        elif q_out.shape != shape:
+            _refuse(q_out, "q_out", torch.bfloat16, shape)
+        qop, qos = _head_rows(q_out, "q_out", dev)
+    elif heads.q_heads or q_out is not None:
+        raise OQError(OQ_ERR_INVALID_ARG, f"q: missing, with {heads.q_heads} heads")
+    if k is not None:
+        shape = k.shape
+        if lead is None:
+            lead = shape[:-2]
+        if shape != (*lead, heads.k_heads, heads.head_dim):
+            _refuse(k, "k", torch.bfloat16, (*lead, heads.k_heads, heads.head_dim))
+        kp, ks = _head_rows(k, "k", dev)
+        if k_out is None:
+            k_out = k.new_empty(shape)
+        elif k_out.shape != shape:
+            _refuse(k_out, "k_out", torch.bfloat16, shape)
+        kop, kos = _head_rows(k_out, "k_out", dev)
+    elif heads.k_heads or k_out is not None:
+        raise OQError(OQ_ERR_INVALID_ARG, f"k: missing, with {heads.k_heads} heads")
     if lead is None:
         raise OQError(OQ_ERR_INVALID_ARG, "neither q nor k given")
     B, S = lead if len(lead) == 2 else (1, lead[0])
-    pos, pbs = _positions(positions, B, S)
-    (qp, qs, qo, qos, q_out), (kp, ks, ko, kos, k_out) = io
-    _check(lib().oq_qk_norm_rope(heads._ref, B, S, qp, qs, kp, ks, pos, pbs, qo, qos, ko, kos,
-                                 _stream(stream)))
+    pos, pbs = _positions(positions, B, S, dev)
+    _check(lib().oq_qk_norm_rope(heads._ref, B, S, qp, qs, kp, ks, pos, pbs, qop, qos, kop, kos,
+                                 _raw_stream(stream, dev)))
     return q_out, k_out
 
 
@@ -684,28 +701,29 @@ def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None
     [N, d] of prepare_weights_w8, or uint8 [N, d/2] of prepare_weights. positions: int32 [S] or
     [batch, S], as for qk_norm_rope; a [B, S] tensor also sets the batch."""
     import torch
-    f32 = torch.float32
-    _check_heads_device(heads)
-    xp, ldx = _need_rows(x, "x", plan.d)
-    w8 = w.dtype == torch.int8
-    wp = _need(w, "w", torch.int8 if w8 else torch.uint8, 2)
-    T, N = x.shape[0], w.shape[0]
-    if w.shape[1] != (plan.d if w8 else plan.d // 2):
-        raise OQError(OQ_ERR_INVALID_ARG, f"w: {w.shape[1]} columns for plan d={plan.d}")
+    f32, bf16, dev = torch.float32, torch.bfloat16, _device()
+    heads._check_device(dev)
+    xp, T, ldx = _need_rows(x, "x", bf16, plan.d, dev)
+    w8 = w.dtype is torch.int8
+    wp, N, Kw = _need_2d(w, "w", torch.int8 if w8 else torch.uint8, dev)
+    if Kw != (plan.d if w8 else plan.d // 2):
+        raise OQError(OQ_ERR_INVALID_ARG, f"w: {Kw} columns for plan d={plan.d}")
     if positions is not None and positions.dim() == 2:
         batch = positions.shape[0]
     if batch < 1 or T % batch:
         raise OQError(OQ_ERR_INVALID_ARG, f"{T} tokens are not {batch} sequences of one length")
     S = T // batch
-    pos, pbs = _positions(positions, batch, S)
-    out = _need_out(out, (T, N), torch.bfloat16, x.device)
-    kind = W_INT8 if w8 else W_INT4
-    need = lib().oq_linear_qkv_workspace_bytes(plan.handle, heads._ref, kind, T, N)
-    workspace, nbytes = _scratch(workspace, need, x.device, stream)
-    _check(lib().oq_linear_qkv(
-        plan.handle, heads._ref, xp, batch, S, ldx, kind, wp, _need_vec(w_scale, "w_scale", f32, N),
-        _need_vec(w_rowsum, "w_rowsum", f32, N), _need_vec(bias, "bias", torch.bfloat16, N), N,
-        pos, pbs, out.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream)))
+    pos, pbs = _positions(positions, batch, S, dev)
+    if out is None:
+        out = x.new_empty((T, N))
+    L, kind = lib(), W_INT8 if w8 else W_INT4
+    need = L.oq_linear_qkv_workspace_bytes(plan.handle, heads._ref, kind, T, N)
+    ws, nbytes, keep = _scratch(workspace, need, x, stream)
+    _check(L.oq_linear_qkv(
+        plan.handle, heads._ref, xp, batch, S, ldx, kind, wp,
+        _need(w_scale, "w_scale", f32, (N,), dev), _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev),
+        _need_opt(bias, "bias", bf16, (N,), dev), N, pos, pbs, _need(out, "out", bf16, (T, N), dev),
+        ws, nbytes, _raw_stream(stream, dev)))
     return out
 
 
