@@ -397,14 +397,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
 // CTA pairs that are resident at once, per kernel and device (0 if the query fails).
 int resident_pairs(const void* kern, int smem, int threads) {
   static std::mutex mu;
@@ -625,7 +617,7 @@ void launch_rows(const RowParams& p, cudaStream_t s) {
   // 4096 x 12288 13.7 against 14.6, 1920 x 5760 (24 tokens) 6.4 against 8.0.
   const unsigned grid = (unsigned)(p.w.N / 16);
   constexpr int D = NT == 1 ? 2 : 1;
-  if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)sm_count())
+  if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)device_sms())
     k_gemm_w8_rows<NT, 2 * D, 2><<<grid, RT, 0, s>>>(p);
   else
     k_gemm_w8_rows<NT, D, 3><<<grid, RT, 0, s>>>(p);
@@ -852,7 +844,7 @@ oq_status run_split(const W8Params& w, cudaStream_t s) {
   p.tcols = 32;
   while (p.tcols < p.npad) p.tcols *= 2;
   p.nkb = (w.K + 127) / 128;
-  const int tiles = (w.N + PM - 1) / PM, sms = sm_count();
+  const int tiles = (w.N + PM - 1) / PM, sms = device_sms();
   // The split that leaves the fullest SM the fewest K blocks; of equal ones the smallest. A further
   // CTA in the cluster costs about as much as a sixteenth of a K block's time in barriers.
   int best = 1, ks = p.nkb;

@@ -46,6 +46,14 @@ unsigned long long* device_error_word() {
   return ptrs[dev];
 }
 
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
 cudaError_t allow_max_dynamic_smem(const void* fn) {
   static std::mutex mu;
   static std::vector<std::pair<int, const void*>> done;

@@ -45,6 +45,9 @@ void lloyd_max_newton_256(double c256[256], double t255[255]);
 // size of any one launch.
 cudaError_t allow_max_dynamic_smem(const void* fn);
 
+// SMs of the current device (148 if it cannot be asked).
+int device_sms();
+
 // ---- errors ------------------------------------------------------------------------------
 oq_status fail(oq_status s, const char* fmt, ...);
 oq_status cuda_fail(cudaError_t e, const char* what);
