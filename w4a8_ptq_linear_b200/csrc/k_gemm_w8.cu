@@ -84,7 +84,7 @@ __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatil
 // 4096 x 12288). What does not fill a wave is cut into narrower tiles, one to a pair.
 constexpr int TM = 128;                    // tokens per CTA
 constexpr int TN = 256;                    // channels per tile at most
-constexpr int CH = 64;                     // channels per chunk
+constexpr int CH = 64;                     // channels per chunk, where no heads are formed
 constexpr int KS = 2;                      // 128-byte K blocks per stage
 constexpr int SK = 3;                      // stages
 constexpr int AK = TM * 128;               // activation bytes of a K block
@@ -95,14 +95,27 @@ constexpr int NEPI = 256;                  // epilogue threads, two warps to a T
 constexpr int NTHR = 128 + NEPI;
 constexpr int OFF_B = SK * AB;
 constexpr int OFF_COL = OFF_B + SK * BB;   // [2][3][TN] floats
-constexpr int OFF_BAR = OFF_COL + 2 * 3 * TN * 4;
+constexpr int OFF_HEAD = OFF_COL + 2 * 3 * TN * 4;   // [4][TN] floats: q, k weights, q, k biases
+constexpr int OFF_BAR = OFF_HEAD + 4 * TN * 4;
 constexpr int NBAR = 2 * SK + 5;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
 
+// Heads formed in the epilogue (columns o < w.n_head): the parameters of HeadArgs
+struct TileHeads {
+  int D, nq, norm, rope, rot;              // nq: query columns
+  float eps, inv_d;
+  const float *qw, *qb, *kw, *kb, *cos, *sin;
+  int64_t n_pos, pos_bs;
+  int seq;
+  const int32_t* positions;
+};
+
 struct TileParams {
   W8Params w;
+  TileHeads h;
+  int cw, maxch;                           // channels of a chunk, chunks of a tile at most
   int npm;                                 // chunks of a token block
   int blocks, ncol, gm;                    // token blocks, tiles of a block, blocks of a group
   int total, full;                         // tiles; those run whole
@@ -158,15 +171,17 @@ __device__ __forceinline__ uint32_t pack2(float2 y) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// y of a token's 32 neighbouring channels: c = fma(mean, w1, b), y = fma(acc, alpha s, c). The
+// y of a token's NF neighbouring channels: c = fma(mean, w1, b), y = fma(acc, alpha s, c). The
 // channels' constants lie at cs (scales), cs + TN (row sums) and cs + 2 TN (biases) floats, the last
 // two read only where they count: shared memory is what the mainloop is short of.
-__device__ __forceinline__ void dequant32(const uint32_t (&r)[32], float alpha, float mean,
-                                          const float4* cs, bool has_mean, bool has_bias,
-                                          float2 (&y)[16]) {
+template <int NF>
+__device__ __forceinline__ void dequant(const uint32_t (&r)[NF], float alpha, float mean,
+                                        const float* col, bool has_mean, bool has_bias,
+                                        float2 (&y)[NF / 2]) {
+  const float4* cs = reinterpret_cast<const float4*>(col);
   const float2 al = make_float2(alpha, alpha), mn = make_float2(mean, mean);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NF / 4; ++i) {
     float4 w4 = make_float4(0.f, 0.f, 0.f, 0.f), b4 = w4;
     const float4 s4 = cs[i];
     if (has_mean) w4 = cs[TN / 4 + i];
@@ -180,6 +195,148 @@ __device__ __forceinline__ void dequant32(const uint32_t (&r)[32], float alpha, 
   }
 }
 
+// The bf16 results of 16 channels
+__device__ __forceinline__ void store_bf16x16(const W8Params& p, int t, int o, const float2* y) {
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = pack2(y[i]);
+  store32(reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t * p.N + o, v, p.wide);
+}
+
+// One query or key head of the warp's 32 tokens, a token to a lane, from its D accumulator columns
+// at `acc`: norm, weight, bias, rotation. The sums of the norm need no exchange; the columns
+// are read from TMEM again for every pass (sum, squares, result) rather than held. D and rot are
+// multiples of 32. The angles of the next 16 pairs are on their way while 16 are turned.
+__device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc, const float* col,
+                                              const float* s_head, int t, int o, float alpha,
+                                              float mean, int64_t pos) {
+  const W8Params& p = tp.w;
+  const TileHeads& h = tp.h;
+  const bool has_mean = p.mean != nullptr, has_bias = p.bias != nullptr, row = t < p.T;
+  const bool is_q = o < h.nq;
+  const float* wt = s_head + (is_q ? 0 : TN);
+  const float* bs = s_head + (is_q ? 2 * TN : 3 * TN);
+  const int half = h.rot / 2;
+  const bool turn = row && pos >= 0, lost = pos >= h.n_pos;
+  float4 cs[4], sn[4];
+  auto angles = [&](int i) {   // of pairs i .. i + 15
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cs[j] = make_float4(1.f, 1.f, 1.f, 1.f);
+      sn[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (turn && !lost && i < half) {
+        cs[j] = __ldg(reinterpret_cast<const float4*>(h.cos + pos * half + i) + j);
+        sn[j] = __ldg(reinterpret_cast<const float4*>(h.sin + pos * half + i) + j);
+      }
+      if (turn && lost) {
+        const float n = __int_as_float(0x7fc00000);
+        cs[j] = sn[j] = make_float4(n, n, n, n);
+      }
+    }
+  };
+  angles(0);
+
+  float m = 0.f, r = 1.f;
+  uint32_t v[32];
+  float2 y[16];
+  if (h.norm == OQ_NORM_LAYER) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < h.D; c += 32) {
+      dev::tmem_ld32(acc + (uint32_t)c, v);
+      dev::tmem_wait_ld();
+      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum = __fadd2_rn(sum, y[i]);
+    }
+    m = (sum.x + sum.y) * h.inv_d;
+  }
+  const float2 neg = make_float2(-m, -m);
+  if (h.norm != OQ_NORM_NONE) {
+    float2 sq = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int c = 0; c < h.D; c += 32) {
+      dev::tmem_ld32(acc + (uint32_t)c, v);
+      dev::tmem_wait_ld();
+      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 d = __fadd2_rn(y[i], neg);
+        sq = __ffma2_rn(d, d, sq);
+      }
+    }
+    r = rsqrtf(fmaf(sq.x + sq.y, h.inv_d, h.eps));
+  }
+  const float2 r2 = make_float2(r, r);
+  auto normed = [&](float2 x, int c) {   // of columns c, c + 1
+    const float2 w2 = *reinterpret_cast<const float2*>(wt + c);
+    const float2 b2 = *reinterpret_cast<const float2*>(bs + c);
+    return __ffma2_rn(__fmul2_rn(__fadd2_rn(x, neg), r2), w2, b2);
+  };
+  if (h.rope == OQ_ROPE_HALVES) {
+#pragma unroll 1
+    for (int i = 0; i < half; i += 16) {
+      uint32_t a[16], d[16];
+      dev::tmem_ld16(acc + (uint32_t)i, a);
+      dev::tmem_ld16(acc + (uint32_t)(i + half), d);
+      dev::tmem_wait_ld();
+      float2 u[8], w[8];
+      dequant<16>(a, alpha, mean, col + i, has_mean, has_bias, u);
+      dequant<16>(d, alpha, mean, col + i + half, has_mean, has_bias, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 nu = normed(u[j], i + 2 * j), nw = normed(w[j], i + half + 2 * j);
+        const float4 c4 = cs[j / 2], s4 = sn[j / 2];
+        const float2 c2 = j & 1 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+        const float2 s2 = j & 1 ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+        const float2 ru = __ffma2_rn(nu, c2, __fmul2_rn(make_float2(-nw.x, -nw.y), s2));
+        const float2 rw = __ffma2_rn(nw, c2, __fmul2_rn(nu, s2));
+        u[j] = turn ? ru : nu;
+        w[j] = turn ? rw : nw;
+      }
+      angles(i + 16);
+      if (row) {
+        store_bf16x16(p, t, o + i, u);
+        store_bf16x16(p, t, o + i + half, w);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < h.rot; c += 32) {
+      dev::tmem_ld32(acc + (uint32_t)c, v);
+      dev::tmem_wait_ld();
+      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 n = normed(y[j], c + 2 * j);
+        const float4 c4 = cs[j / 4], s4 = sn[j / 4];
+        const float cc = j % 4 == 0 ? c4.x : j % 4 == 1 ? c4.y : j % 4 == 2 ? c4.z : c4.w;
+        const float ss = j % 4 == 0 ? s4.x : j % 4 == 1 ? s4.y : j % 4 == 2 ? s4.z : s4.w;
+        y[j] = turn ? make_float2(n.x * cc - n.y * ss, n.x * ss + n.y * cc) : n;
+      }
+      angles((c + 32) / 2);
+      if (row) {
+        store_bf16x16(p, t, o + c, y);
+        store_bf16x16(p, t, o + c + 16, y + 8);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int c = h.rot; c < h.D; c += 32) {   // elements that no rotation reaches
+    dev::tmem_ld32(acc + (uint32_t)c, v);
+    dev::tmem_wait_ld();
+    dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] = normed(y[j], c + 2 * j);
+    if (row) {
+      store_bf16x16(p, t, o + c, y);
+      store_bf16x16(p, t, o + c + 16, y + 8);
+    }
+  }
+}
+
+// HEADS: query and key heads are formed in the epilogue (tp.h); tiles then hold whole heads.
+template <bool HEADS>
 __global__ void __launch_bounds__(NTHR, 1)
     k_gemm_w8(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ TileParams tp) {
@@ -221,6 +378,15 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
   if (warp == 0 && lane == 0) dev::prefetch_tmap(&tm_a);
   if (warp == 2 && lane == 0) dev::prefetch_tmap(&tm_b);
+  if constexpr (HEADS) {
+    float* s_head = reinterpret_cast<float*>(smem + OFF_HEAD);
+    for (int i = tid; i < tp.h.D; i += NTHR) {
+      s_head[i] = tp.h.qw ? tp.h.qw[i] : 1.f;
+      s_head[TN + i] = tp.h.kw ? tp.h.kw[i] : 1.f;
+      s_head[2 * TN + i] = tp.h.qb ? tp.h.qb[i] : 0.f;
+      s_head[3 * TN + i] = tp.h.kb ? tp.h.kb[i] : 0.f;
+    }
+  }
   if (warp == 1) {
     dev::tmem_alloc_pair(dev::smem_u32(&s_misc[0]), 2 * TN);
     dev::tmem_relinquish_pair();
@@ -229,6 +395,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   dev::cluster_sync();   // barrier inits of both CTAs visible before any remote arrive
   dev::tc_fence_after();
   const uint32_t tmem = s_misc[0];
+  const int cw = HEADS ? tp.cw : CH;   // channels of a chunk
   Tiles it(tp, unit, (int)gridDim.x / 2);
   int m, c0, nch;
 
@@ -240,10 +407,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       Ring rg;
       bool ok = true;
       while (ok && it.next(m, c0, nch)) {
-        const int rows = nch * CH / 2;                      // this CTA's weight rows
+        const int rows = nch * cw / 2;                      // this CTA's weight rows
         const int boxes = tok ? 1 : (rows + BBOX - 1) / BBOX;
         const uint32_t block_bytes = tok ? 2u * AK : 2u * boxes * BBOX * 128u;   // of both CTAs
-        const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * CH + (int)rank * rows;
+        const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * cw + (int)rank * rows;
         for (int st = 0; st < nst; ++st, ++j, rg.next(SK)) {
           const int s = rg.st, nk = min(KS, nkb - st * KS);
           if (!ring_wait(free_bar(s), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) {
@@ -282,7 +449,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       Ring rg;
       bool ok = true, issued = false;
       for (; ok && it.next(m, c0, nch); ++n) {
-        const uint32_t idesc = dev::idesc_i8(2 * TM, nch * CH);
+        const uint32_t idesc = dev::idesc_i8(2 * TM, nch * cw);
         const int b = n & 1;
         if (!ring_wait(tempty_bar(b), ((n >> 1) & 1u) ^ 1u, s_abort, p, kSiteGemmAccum)) {
           ok = false;
@@ -323,7 +490,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     uint32_t n = 0;
     bool ok = true;
     for (; ok && it.next(m, c0, nch); ++n) {
-      const int b = n & 1, ncols = nch * CH, o0 = c0 * CH;
+      const int b = n & 1, ncols = nch * cw, o0 = c0 * cw;
       const int tw = (2 * m + (int)rank) * TM + q * 32, t = tw + lane;   // tokens of the warp
       float* col = s_col + b * 3 * TN;
       for (int i = etid; i < ncols; i += NEPI) {
@@ -348,37 +515,58 @@ __global__ void __launch_bounds__(NTHR, 1)
       ok = *reinterpret_cast<volatile uint32_t*>(&s_misc[2 + b]) != 0;
       dev::tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * TN);
-#pragma unroll 1
-      for (int c = half; ok && c < nch * (CH / 32); c += 2) {
-        uint32_t r[32];
-        dev::tmem_ld32(acc + (uint32_t)(c * 32), r);
-        dev::tmem_wait_ld();
-        const int o = o0 + c * 32;
-        if (t >= p.T || o >= p.N) continue;   // no warp-wide step below
-        const bool two = o + 16 < p.N;        // N % 16 == 0: sixteen or all of the channels
-        if (p.out_acc) {
-          int32_t* dst = reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < 2 || two) store32(dst + 8 * i, r + 8 * i, p.wide);
-          continue;
+      // Heads: a chunk is a head or, behind them, as many plain columns; the two warps of a lane
+      // quarter take chunks in turn. Else they take 32 columns in turn.
+      int first = half, step = 2, last = ncols / 32, pieces = 0;
+      int64_t pos = -1;
+      if constexpr (HEADS) {
+        first = 0, last = 0;
+        if (t < p.T) {
+          const int bt = t / tp.h.seq, st = t - bt * tp.h.seq;
+          pos = tp.h.positions ? (int64_t)tp.h.positions[bt * tp.h.pos_bs + st] : st;
         }
-        float2 y[16];
-        const float4* cs = reinterpret_cast<const float4*>(col + c * 32);
-        dequant32(r, alpha, mean, cs, p.mean != nullptr, p.bias != nullptr, y);
+        pieces = nch;
+      }
+#pragma unroll 1
+      for (int ch = half; HEADS ? ok && ch < pieces : ch == half; ch += 2) {
+        if constexpr (HEADS) {
+          if (tw >= p.T || o0 + ch * cw >= p.N) continue;   // warp-uniform
+          if (o0 + ch * cw < p.n_head) {
+            head_epilogue(tp, acc + (uint32_t)(ch * cw), col + ch * cw,
+                          reinterpret_cast<const float*>(smem + OFF_HEAD), t, o0 + ch * cw, alpha,
+                          mean, pos);
+            continue;
+          }
+          first = ch * cw / 32, step = 1, last = (ch + 1) * cw / 32;
+        }
+#pragma unroll 1
+        for (int c = first; ok && c < last; c += step) {
+          uint32_t r[32];
+          dev::tmem_ld32(acc + (uint32_t)(c * 32), r);
+          dev::tmem_wait_ld();
+          const int o = o0 + c * 32;
+          if (t >= p.T || o >= p.N) continue;   // no warp-wide step below
+          const bool two = o + 16 < p.N;        // N % 16 == 0: sixteen or all of the channels
+          if (!HEADS && p.out_acc) {
+            int32_t* dst = reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int oh = o + h * 16;
-          if (h && !two) break;
-          if (oh < p.n_head) {   // n_head % 16 == 0
-            float* dst = p.head + (int64_t)t * p.n_head + oh;
-            store32(dst, reinterpret_cast<const uint32_t*>(y + h * 8), true);
-            store32(dst + 8, reinterpret_cast<const uint32_t*>(y + h * 8 + 4), true);
-          } else {
-            uint32_t v[8];
+            for (int i = 0; i < 4; ++i)
+              if (i < 2 || two) store32(dst + 8 * i, r + 8 * i, p.wide);
+            continue;
+          }
+          float2 y[16];
+          dequant<32>(r, alpha, mean, col + c * 32, p.mean != nullptr, p.bias != nullptr, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = pack2(y[h * 8 + i]);
-            store32(reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t * p.N + oh, v, p.wide);
+          for (int h = 0; h < 2; ++h) {
+            const int oh = o + h * 16;
+            if (h && !two) break;
+            if (!HEADS && oh < p.n_head) {   // n_head % 16 == 0
+              float* dst = p.head + (int64_t)t * p.n_head + oh;
+              store32(dst, reinterpret_cast<const uint32_t*>(y + h * 8), true);
+              store32(dst + 8, reinterpret_cast<const uint32_t*>(y + h * 8 + 4), true);
+            } else {
+              store_bf16x16(p, t, oh, y + h * 8);
+            }
           }
         }
       }
@@ -426,7 +614,7 @@ int resident_pairs(const void* kern, int smem, int threads) {
   return n;
 }
 
-oq_status run_tiles(const W8Params& w, cudaStream_t s) {
+oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   CUtensorMap ta, tb;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
   const bool ok = tma_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.a, K, T, K, 128, TM,
@@ -434,16 +622,30 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
                   tma_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, BBOX,
                              CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return fail(OQ_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable");
-  const auto kern = &k_gemm_w8;
+  const auto kern = heads ? &k_gemm_w8<true> : &k_gemm_w8<false>;
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8)");
   int units = resident_pairs(reinterpret_cast<const void*>(kern), SMEM, NTHR);
   if (units <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no CTA pair fits on this device");
   TileParams p{};
   p.w = w;
-  p.npm = (w.N + CH - 1) / CH;
+  p.cw = CH;
+  if (heads) {
+    p.cw = heads->head_dim;
+    p.h.D = heads->head_dim; p.h.nq = heads->q.heads * heads->head_dim;
+    p.h.norm = heads->norm; p.h.rope = heads->rope;
+    p.h.rot = heads->rope == OQ_ROPE_NONE ? 0 : heads->rot_dim;
+    p.h.eps = heads->eps; p.h.inv_d = 1.f / (float)heads->head_dim;
+    p.h.qw = heads->q.weight; p.h.qb = heads->q.bias;
+    p.h.kw = heads->k.weight; p.h.kb = heads->k.bias;
+    p.h.cos = heads->cos; p.h.sin = heads->sin; p.h.n_pos = heads->n_pos;
+    p.h.positions = heads->positions; p.h.pos_bs = heads->pos_batch_stride;
+    p.h.seq = (int)heads->seq;
+  }
+  p.maxch = TN / p.cw;
+  p.npm = (w.N + p.cw - 1) / p.cw;
   const int64_t blocks = ((int64_t)w.T + 2 * TM - 1) / (2 * TM);
-  p.ncol = (p.npm * CH + TN - 1) / TN;
+  p.ncol = (p.npm + p.maxch - 1) / p.maxch;
   if (blocks * p.ncol > 0x3FFFFFFF)
     return fail(OQ_ERR_INVALID_ARG, "gemm_w8: T x d_out too large for one call");
   p.blocks = (int)blocks;
@@ -452,7 +654,7 @@ oq_status run_tiles(const W8Params& w, cudaStream_t s) {
   p.gm = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, (32 << 20) / (2 * TM * (int64_t)w.K)));
   p.full = p.total / units * units;
   const int rest = p.total - p.full;
-  p.split = rest ? std::min(units / rest, TN / CH) : 1;
+  p.split = rest ? std::min(units / rest, p.maxch) : 1;
   if (p.full == 0) units = rest * p.split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2u * (unsigned)units);
@@ -891,6 +1093,10 @@ oq_status run_split(const W8Params& w, cudaStream_t s) {
 
 }  // namespace
 
+bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim) {
+  return T > kSplitTokens && head_dim % 32 == 0 && (rope == OQ_ROPE_NONE || rot_dim % 32 == 0);
+}
+
 oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   if (g.T == 0) return OQ_OK;
   W8Params p{};
@@ -904,7 +1110,7 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.limit_ns = kWaitLimitNs;
   if (g.T <= kRowTokens) return run_rows(p, s);
   if (g.T <= kSplitTokens) return run_split(p, s);
-  return run_tiles(p, s);
+  return run_tiles(p, g.heads, s);
 }
 
 }  // namespace oq

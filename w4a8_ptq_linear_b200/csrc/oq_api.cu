@@ -826,11 +826,12 @@ oq_status oq_gemm_w8a8(const int8_t* a, const float* a_scale, const float* mean,
   return launch_gemm_w8(g, static_cast<cudaStream_t>(stream));
 }
 
-// The INT8-weight layer; with `head` the first n_head columns go there in float32.
+// The INT8-weight layer; the first n_head columns go to `head` in float32 or are formed into `heads`.
 static oq_status linear_w8a8_impl(const oq_plan* plan, const void* x, int64_t T, int64_t ldx,
                                   const int8_t* w, const float* w_scale, const float* w_rowsum,
                                   const void* bias, int64_t d_out, void* y, void* workspace,
-                                  float* head, int64_t n_head, void* stream) {
+                                  float* head, int64_t n_head, const HeadArgs* heads,
+                                  void* stream) {
   const size_t code_bytes = linear_code_bytes(plan, T);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* scale = reinterpret_cast<float*>(ws + round256(code_bytes));
@@ -847,7 +848,7 @@ static oq_status linear_w8a8_impl(const oq_plan* plan, const void* x, int64_t T,
   g.a = reinterpret_cast<const int8_t*>(ws); g.a_scale = scale;
   g.mean = plan->center ? mean : nullptr;
   g.w = w; g.w_scale = w_scale; g.w_rowsum = w_rowsum; g.bias = bias; g.T = T; g.K = plan->d;
-  g.N = d_out; g.out = y; g.head = head; g.n_head = n_head;
+  g.N = d_out; g.out = y; g.head = head; g.n_head = n_head; g.heads = heads;
   return launch_gemm_w8(g, static_cast<cudaStream_t>(stream));
 }
 
@@ -874,7 +875,7 @@ oq_status oq_linear_w8a8(const oq_plan* plan, const void* x_bf16, int64_t T, int
                              oq_linear_workspace_bytes(plan, T));
   if (st != OQ_OK) return st;
   return linear_w8a8_impl(plan, x_bf16, T, ldx, w_codes, w_scale, w_rowsum, bias_bf16, d_out,
-                          y_bf16, workspace, nullptr, 0, stream);
+                          y_bf16, workspace, nullptr, 0, nullptr, stream);
 }
 
 oq_status oq_qk_norm_rope(const oq_heads* heads, int64_t batch, int64_t seq, const void* q,
@@ -906,9 +907,13 @@ oq_status oq_qk_norm_rope(const oq_heads* heads, int64_t batch, int64_t seq, con
   return launch_heads(a, static_cast<cudaStream_t>(stream));
 }
 
-// float32 query and key columns of the INT8 projection, behind the layer's own workspace
+// The INT8 projection forms the heads in the GEMM's epilogue where it can.
+static bool heads_in_gemm(const oq_heads* h, oq_weight_kind weights, int64_t T) {
+  return weights == OQ_W_INT8 && gemm_w8_forms_heads(T, h->head_dim, h->rope, h->rot_dim);
+}
+// else its float32 query and key columns lie behind the layer's own workspace
 static size_t head_bytes(const oq_heads* h, oq_weight_kind weights, int64_t T) {
-  return weights == OQ_W_INT8
+  return weights == OQ_W_INT8 && !heads_in_gemm(h, weights, T)
              ? round256((size_t)T * (size_t)(h->q_heads + h->k_heads) * h->head_dim * 4)
              : 0;
 }
@@ -951,16 +956,19 @@ oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* 
   if (!y_bf16 || !aligned16(y_bf16))
     return fail(y_bf16 ? OQ_ERR_MISALIGNED : OQ_ERR_INVALID_ARG, "y must be given, 16-byte aligned");
   const size_t layer = oq_linear_workspace_bytes(plan, T);
+  HeadArgs a = head_args(heads, batch, seq, positions, pos_batch_stride);
+  if (heads_in_gemm(heads, weights, T))
+    return linear_w8a8_impl(plan, x_bf16, T, ldx, static_cast<const int8_t*>(w), w_scale, w_rowsum,
+                            bias_bf16, d_out, y_bf16, workspace, nullptr, n_head, &a, stream);
   float* head = weights == OQ_W_INT8
                     ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + layer) : nullptr;
   if (weights == OQ_W_INT8)
     st = linear_w8a8_impl(plan, x_bf16, T, ldx, static_cast<const int8_t*>(w), w_scale, w_rowsum,
-                          bias_bf16, d_out, y_bf16, workspace, head, n_head, stream);
+                          bias_bf16, d_out, y_bf16, workspace, head, n_head, nullptr, stream);
   else
     st = oq_linear(plan, x_bf16, T, ldx, static_cast<const uint8_t*>(w), w_scale, w_rowsum,
                    bias_bf16, d_out, y_bf16, workspace, layer, stream);
   if (st != OQ_OK) return st;
-  HeadArgs a = head_args(heads, batch, seq, positions, pos_batch_stride);
   const int64_t ld = head ? n_head : d_out;
   const int esz = head ? 4 : 2;
   a.in_f32 = head != nullptr;

@@ -157,23 +157,6 @@ oq_status launch_linear_fused(const FusedArgs& a, cudaStream_t s);
 // launch wrote; OQ_ERR_UNSUPPORTED (nothing launched) outside that or when it does not fit.
 oq_status launch_gemm_splitk(const GemmArgs& g, cudaStream_t s);
 
-// ---- INT8 weights (k_gemm_w8.cu) ---------------------------------------------------------
-struct GemmW8Args {
-  const int8_t* a = nullptr;        // int8 [T, K]
-  const float* a_scale = nullptr;
-  const float* mean = nullptr;      // may be null
-  const int8_t* w = nullptr;        // int8 [N, K]
-  const float* w_scale = nullptr;
-  const float* w_rowsum = nullptr;  // may be null when mean is null
-  const void* bias = nullptr;       // bf16 [N] or null
-  int64_t T = 0, K = 0, N = 0;
-  int out_acc = 0;
-  void* out = nullptr;              // bf16 [T, N], or int32 [T, N] with out_acc
-  float* head = nullptr;            // float [T, n_head]: columns o < n_head go here, unrounded,
-  int64_t n_head = 0;               // instead of to out (bf16 output only)
-};
-oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s);
-
 // ---- head norms and position rotation (k_heads.cu) -------------------------------------------
 struct HeadIo {                     // one of q, k
   const void* in = nullptr;         // bf16, or float with HeadArgs::in_f32
@@ -196,6 +179,28 @@ struct HeadArgs {
   int64_t pos_batch_stride = 0;
 };
 oq_status launch_heads(const HeadArgs& a, cudaStream_t s);
+
+// ---- INT8 weights (k_gemm_w8.cu) ---------------------------------------------------------
+struct GemmW8Args {
+  const int8_t* a = nullptr;        // int8 [T, K]
+  const float* a_scale = nullptr;
+  const float* mean = nullptr;      // may be null
+  const int8_t* w = nullptr;        // int8 [N, K]
+  const float* w_scale = nullptr;
+  const float* w_rowsum = nullptr;  // may be null when mean is null
+  const void* bias = nullptr;       // bf16 [N] or null
+  int64_t T = 0, K = 0, N = 0;
+  int out_acc = 0;
+  void* out = nullptr;              // bf16 [T, N], or int32 [T, N] with out_acc
+  // bf16 output only: the columns o < n_head either go to `head`, float [T, n_head], unrounded,
+  // instead of to out, or (heads given) are query and key heads that the epilogue forms
+  float* head = nullptr;
+  int64_t n_head = 0;
+  const HeadArgs* heads = nullptr;
+};
+oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s);
+// Whether the GEMM for T tokens can form these heads in its epilogue.
+bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim);
 
 // oq_prepare_weights that also writes the rotated rows (float [n_out, d]) to `rot` (if not null)
 oq_status oq_prepare_weights_rotated(const oq_plan* plan, const void* w_bf16, int64_t n_out,
