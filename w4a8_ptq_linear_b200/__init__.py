@@ -626,16 +626,18 @@ class Heads:
                                               f"device is {dev}")
 
 
-_Strides = _I64 * 3
+_Strides = _I64 * 12
 
 
-def _head_rows(t, name, dev):
-    """(pointer, strides) of a bf16 [S, heads, D] or [B, S, heads, D] view, elements contiguous."""
+def _head_rows(t, name, shape, dev):
+    """(pointer, batch, token and head stride) of a bf16 [S, heads, D] or [B, S, heads, D] view
+    of this shape, elements contiguous."""
     import torch
+    if (t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev
+            or t.stride(-1) != 1):
+        _refuse(t, name, torch.bfloat16, shape)
     st = t.stride()
-    if len(st) not in (3, 4) or t.dtype is not torch.bfloat16 or t.get_device() != dev or st[-1] != 1:
-        _refuse(t, name, torch.bfloat16, None if len(st) in (3, 4) else ("[B,] S", "heads", "D"))
-    return t.data_ptr(), _Strides(*st[:3]) if len(st) == 4 else _Strides(0, st[0], st[1])
+    return t.data_ptr(), (st[:3] if len(st) == 4 else (0, st[0], st[1]))
 
 
 def _positions(positions, B, S, dev):
@@ -656,42 +658,34 @@ def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, 
     import torch
     dev = _device()
     heads._check_device(dev)
-    lead = None
-    qp = qs = qop = qos = kp = ks = kop = kos = None
-    if q is not None:
-        shape = q.shape
-        lead = shape[:-2]
-        if shape != (*lead, heads.q_heads, heads.head_dim):
-            _refuse(q, "q", torch.bfloat16, ("[B,] S", heads.q_heads, heads.head_dim))
-        qp, qs = _head_rows(q, "q", dev)
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        elif q_out.shape != shape:
-            _refuse(q_out, "q_out", torch.bfloat16, shape)
-        qop, qos = _head_rows(q_out, "q_out", dev)
-    elif heads.q_heads or q_out is not None:
-        raise OQError(OQ_ERR_INVALID_ARG, f"q: missing, with {heads.q_heads} heads")
-    if k is not None:
-        shape = k.shape
-        if lead is None:
-            lead = shape[:-2]
-        if shape != (*lead, heads.k_heads, heads.head_dim):
-            _refuse(k, "k", torch.bfloat16, (*lead, heads.k_heads, heads.head_dim))
-        kp, ks = _head_rows(k, "k", dev)
-        if k_out is None:
-            k_out = k.new_empty(shape)
-        elif k_out.shape != shape:
-            _refuse(k_out, "k_out", torch.bfloat16, shape)
-        kop, kos = _head_rows(k_out, "k_out", dev)
-    elif heads.k_heads or k_out is not None:
-        raise OQError(OQ_ERR_INVALID_ARG, f"k: missing, with {heads.k_heads} heads")
-    if lead is None:
+    first = q if q is not None else k
+    if first is None:
         raise OQError(OQ_ERR_INVALID_ARG, "neither q nor k given")
+    lead = tuple(first.shape[:-2])
+    if len(lead) not in (1, 2):
+        _refuse(first, "q" if q is not None else "k", torch.bfloat16, ("[B,] S", "heads", "D"))
+    at, strides = [], ()
+    for t, o, name, n in ((q, q_out, "q", heads.q_heads), (k, k_out, "k", heads.k_heads)):
+        if t is None:
+            if n or o is not None:
+                raise OQError(OQ_ERR_INVALID_ARG, f"{name}: missing, with {n} heads")
+            at += (None, None, None)
+            strides += (0, 0, 0, 0, 0, 0)
+            continue
+        shape = (*lead, n, heads.head_dim)
+        ptr, st = _head_rows(t, name, shape, dev)
+        if o is None:
+            o = t.new_empty(shape)
+        optr, ost = _head_rows(o, name + "_out", shape, dev)
+        at += (ptr, optr, o)
+        strides += (*st, *ost)
     B, S = lead if len(lead) == 2 else (1, lead[0])
     pos, pbs = _positions(positions, B, S, dev)
-    _check(lib().oq_qk_norm_rope(heads._ref, B, S, qp, qs, kp, ks, pos, pbs, qop, qos, kop, kos,
-                                 _raw_stream(stream, dev)))
-    return q_out, k_out
+    table = _Strides(*strides)                   # q, q_out, k, k_out, three strides each
+    s = ctypes.addressof(table)
+    _check(lib().oq_qk_norm_rope(heads._ref, B, S, at[0], s, at[3], s + 48, pos, pbs, at[1], s + 24,
+                                 at[4], s + 72, _raw_stream(stream, dev)))
+    return at[2], at[5]
 
 
 def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None, *, batch=1,

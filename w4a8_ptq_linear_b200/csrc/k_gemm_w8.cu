@@ -204,74 +204,90 @@ __device__ __forceinline__ void store_bf16x16(const W8Params& p, int t, int o, c
 }
 
 // One query or key head of the warp's 32 tokens, a token to a lane, from its D accumulator columns
-// at `acc`: norm, weight, bias, rotation. The sums of the norm need no exchange; the columns
-// are read from TMEM again for every pass (sum, squares, result) rather than held. D and rot are
-// multiples of 32. The angles of the next 16 pairs are on their way while 16 are turned.
+// at `acc`: norm, weight, bias, rotation. The sums of the norm need no exchange. The first pass puts
+// the float32 values back in TMEM in the sums' place, and the later ones (squares about the mean,
+// result) read them from there: shared memory, which the channels' constants come from, is what
+// the mainloop is short of. D and rot are multiples of 32. The angles of the next 16 pairs are on
+// their way while 16 are turned.
 __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc, const float* col,
                                               const float* s_head, int t, int o, float alpha,
                                               float mean, int64_t pos) {
   const W8Params& p = tp.w;
   const TileHeads& h = tp.h;
-  const bool has_mean = p.mean != nullptr, has_bias = p.bias != nullptr, row = t < p.T;
+  const bool row = t < p.T;
   const bool is_q = o < h.nq;
   const float* wt = s_head + (is_q ? 0 : TN);
   const float* bs = s_head + (is_q ? 2 * TN : 3 * TN);
+  const bool has_wt = (is_q ? h.qw : h.kw) != nullptr, has_bs = (is_q ? h.qb : h.kb) != nullptr;
   const int half = h.rot / 2;
   const bool turn = row && pos >= 0, lost = pos >= h.n_pos;
   float4 cs[4], sn[4];
   auto angles = [&](int i) {   // of pairs i .. i + 15
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      cs[j] = make_float4(1.f, 1.f, 1.f, 1.f);
-      sn[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (turn && !lost && i < half) {
         cs[j] = __ldg(reinterpret_cast<const float4*>(h.cos + pos * half + i) + j);
         sn[j] = __ldg(reinterpret_cast<const float4*>(h.sin + pos * half + i) + j);
-      }
-      if (turn && lost) {
-        const float n = __int_as_float(0x7fc00000);
+      } else {
+        const float n = __int_as_float(0x7fc00000);   // a position past the table, or unused
         cs[j] = sn[j] = make_float4(n, n, n, n);
       }
     }
   };
   angles(0);
 
-  float m = 0.f, r = 1.f;
+  float2 sum = make_float2(0.f, 0.f), sq = sum;
+  const bool layer = h.norm == OQ_NORM_LAYER;
   uint32_t v[32];
   float2 y[16];
-  if (h.norm == OQ_NORM_LAYER) {
-    float2 sum = make_float2(0.f, 0.f);
+  auto floats = [&](int i) {   // of columns 2 i, 2 i + 1 just read
+    return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  };
 #pragma unroll 1
-    for (int c = 0; c < h.D; c += 32) {
-      dev::tmem_ld32(acc + (uint32_t)c, v);
-      dev::tmem_wait_ld();
-      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
+  for (int c = 0; c < h.D; c += 32) {
+    dev::tmem_ld32(acc + (uint32_t)c, v);
+    dev::tmem_wait_ld();
+    dequant<32>(v, alpha, mean, col + c, p.mean != nullptr, p.bias != nullptr, y);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = __fadd2_rn(sum, y[i]);
+    for (int i = 0; i < 16; ++i) {
+      sum = __fadd2_rn(sum, y[i]);
+      sq = __ffma2_rn(y[i], y[i], sq);
+      v[2 * i] = __float_as_uint(y[i].x);
+      v[2 * i + 1] = __float_as_uint(y[i].y);
     }
-    m = (sum.x + sum.y) * h.inv_d;
+    dev::tmem_st32(acc + (uint32_t)c, v);
   }
+  dev::tmem_wait_st();
+  const float m = layer ? (sum.x + sum.y) * h.inv_d : 0.f;
   const float2 neg = make_float2(-m, -m);
-  if (h.norm != OQ_NORM_NONE) {
-    float2 sq = make_float2(0.f, 0.f);
+  if (layer) {
+    sq = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int c = 0; c < h.D; c += 32) {
       dev::tmem_ld32(acc + (uint32_t)c, v);
       dev::tmem_wait_ld();
-      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float2 d = __fadd2_rn(y[i], neg);
+        const float2 d = __fadd2_rn(floats(i), neg);
         sq = __ffma2_rn(d, d, sq);
       }
     }
-    r = rsqrtf(fmaf(sq.x + sq.y, h.inv_d, h.eps));
   }
+  const float r = h.norm == OQ_NORM_NONE ? 1.f : rsqrtf(fmaf(sq.x + sq.y, h.inv_d, h.eps));
   const float2 r2 = make_float2(r, r);
-  auto normed = [&](float2 x, int c) {   // of columns c, c + 1
-    const float2 w2 = *reinterpret_cast<const float2*>(wt + c);
-    const float2 b2 = *reinterpret_cast<const float2*>(bs + c);
-    return __ffma2_rn(__fmul2_rn(__fadd2_rn(x, neg), r2), w2, b2);
+  // N / 2 pairs of columns from c on: norm, weight, bias
+  auto normed = [&](float2* x, int n, int c) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      if (i >= n) break;
+      float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f), b4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (has_wt) w4 = *reinterpret_cast<const float4*>(wt + c + 2 * i);
+      if (has_bs) b4 = *reinterpret_cast<const float4*>(bs + c + 2 * i);
+      x[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[i], neg), r2), make_float2(w4.x, w4.y),
+                        make_float2(b4.x, b4.y));
+      x[i + 1] = __ffma2_rn(__fmul2_rn(__fadd2_rn(x[i + 1], neg), r2), make_float2(w4.z, w4.w),
+                            make_float2(b4.z, b4.w));
+    }
   };
   if (h.rope == OQ_ROPE_HALVES) {
 #pragma unroll 1
@@ -281,18 +297,23 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
       dev::tmem_ld16(acc + (uint32_t)(i + half), d);
       dev::tmem_wait_ld();
       float2 u[8], w[8];
-      dequant<16>(a, alpha, mean, col + i, has_mean, has_bias, u);
-      dequant<16>(d, alpha, mean, col + i + half, has_mean, has_bias, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 nu = normed(u[j], i + 2 * j), nw = normed(w[j], i + half + 2 * j);
-        const float4 c4 = cs[j / 2], s4 = sn[j / 2];
-        const float2 c2 = j & 1 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
-        const float2 s2 = j & 1 ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
-        const float2 ru = __ffma2_rn(nu, c2, __fmul2_rn(make_float2(-nw.x, -nw.y), s2));
-        const float2 rw = __ffma2_rn(nw, c2, __fmul2_rn(nu, s2));
-        u[j] = turn ? ru : nu;
-        w[j] = turn ? rw : nw;
+        u[j] = make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
+        w[j] = make_float2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+      }
+      normed(u, 8, i);
+      normed(w, 8, i + half);
+      if (turn) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 c4 = cs[j / 2], s4 = sn[j / 2];
+          const float2 c2 = j & 1 ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+          const float2 s2 = j & 1 ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+          const float2 ru = __ffma2_rn(u[j], c2, __fmul2_rn(make_float2(-w[j].x, -w[j].y), s2));
+          w[j] = __ffma2_rn(w[j], c2, __fmul2_rn(u[j], s2));
+          u[j] = ru;
+        }
       }
       angles(i + 16);
       if (row) {
@@ -305,14 +326,18 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
     for (int c = 0; c < h.rot; c += 32) {
       dev::tmem_ld32(acc + (uint32_t)c, v);
       dev::tmem_wait_ld();
-      dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 n = normed(y[j], c + 2 * j);
-        const float4 c4 = cs[j / 4], s4 = sn[j / 4];
-        const float cc = j % 4 == 0 ? c4.x : j % 4 == 1 ? c4.y : j % 4 == 2 ? c4.z : c4.w;
-        const float ss = j % 4 == 0 ? s4.x : j % 4 == 1 ? s4.y : j % 4 == 2 ? s4.z : s4.w;
-        y[j] = turn ? make_float2(n.x * cc - n.y * ss, n.x * ss + n.y * cc) : n;
+      for (int j = 0; j < 16; ++j) y[j] = floats(j);
+      normed(y, 16, c);
+      if (turn) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 n = y[j];
+          const float4 c4 = cs[j / 4], s4 = sn[j / 4];
+          const float cc = j % 4 == 0 ? c4.x : j % 4 == 1 ? c4.y : j % 4 == 2 ? c4.z : c4.w;
+          const float ss = j % 4 == 0 ? s4.x : j % 4 == 1 ? s4.y : j % 4 == 2 ? s4.z : s4.w;
+          y[j] = make_float2(n.x * cc - n.y * ss, n.x * ss + n.y * cc);
+        }
       }
       angles((c + 32) / 2);
       if (row) {
@@ -325,9 +350,9 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   for (int c = h.rot; c < h.D; c += 32) {   // elements that no rotation reaches
     dev::tmem_ld32(acc + (uint32_t)c, v);
     dev::tmem_wait_ld();
-    dequant<32>(v, alpha, mean, col + c, has_mean, has_bias, y);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = normed(y[j], c + 2 * j);
+    for (int j = 0; j < 16; ++j) y[j] = floats(j);
+    normed(y, 16, c);
     if (row) {
       store_bf16x16(p, t, o + c, y);
       store_bf16x16(p, t, o + c + 16, y + 8);
