@@ -672,11 +672,14 @@ def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, 
             at += (None, None, None)
             strides += (0, 0, 0, 0, 0, 0)
             continue
-        shape = (*lead, n, heads.head_dim)
+        D = heads.head_dim
+        shape = (*lead, n, D)
         ptr, st = _head_rows(t, name, shape, dev)
         if o is None:
             o = t.new_empty(shape)
-        optr, ost = _head_rows(o, name + "_out", shape, dev)
+            optr, ost = o.data_ptr(), (lead[-1] * n * D, n * D, D)
+        else:
+            optr, ost = _head_rows(o, name + "_out", shape, dev)
         at += (ptr, optr, o)
         strides += (*st, *ost)
     B, S = lead if len(lead) == 2 else (1, lead[0])

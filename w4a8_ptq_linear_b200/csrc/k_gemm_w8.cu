@@ -37,9 +37,20 @@ struct W8Params {
   bool wide;                // out is 32-byte aligned (its rows are: N % 16 == 0)
   void* out;
   float* head;
+  bool dependent;           // launched beside the kernel that writes a, a_scale and mean
   unsigned long long* err;
   unsigned long long limit_ns;
 };
+
+// The launch before (whose results a, a_scale and mean may be) has ended and its writes are visible;
+// at once where the launch is an ordinary one.
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// A launch that waits for this grid may begin beside it.
+__device__ __forceinline__ void dependents_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // A walk over the stages of a ring. One thread issues a role's steps, so its own instructions are on
 // the critical path: a division for the stage and the phase of each step took 0.1 us of it.
@@ -240,8 +251,8 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   const bool layer = h.norm == OQ_NORM_LAYER;
   uint32_t v[32];
   float2 y[16];
-  auto floats = [&](int i) {   // of columns 2 i, 2 i + 1 just read
-    return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  auto floats = [](const uint32_t (&q)[32], int i) {   // columns 2 i, 2 i + 1
+    return make_float2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
   };
 #pragma unroll 1
   for (int c = 0; c < h.D; c += 32) {
@@ -268,7 +279,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
       dev::tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float2 d = __fadd2_rn(floats(i), neg);
+        const float2 d = __fadd2_rn(floats(v, i), neg);
         sq = __ffma2_rn(d, d, sq);
       }
     }
@@ -327,7 +338,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
       dev::tmem_ld32(acc + (uint32_t)c, v);
       dev::tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] = floats(j);
+      for (int j = 0; j < 16; ++j) y[j] = floats(v, j);
       normed(y, 16, c);
       if (turn) {
 #pragma unroll
@@ -351,7 +362,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
     dev::tmem_ld32(acc + (uint32_t)c, v);
     dev::tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = floats(j);
+    for (int j = 0; j < 16; ++j) y[j] = floats(v, j);
     normed(y, 16, c);
     if (row) {
       store_bf16x16(p, t, o + c, y);
@@ -366,6 +377,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     k_gemm_w8(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ TileParams tp) {
   const W8Params& p = tp.w;
+  dependents_begin();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -426,6 +438,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 
   if (warp == 0 || warp == 2) {
     // ---------------- producers: warp 0 the tokens, warp 2 the weights ----------------
+    if (warp == 0) dependency_wait();   // the weights do not come from the launch before
     if (lane == 0) {
       const bool tok = warp == 0;
       uint32_t j = 0;
@@ -511,6 +524,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
   } else if (warp >= 4) {
     // ---------------- epilogue: a lane holds a token ----------------
+    dependency_wait();   // scales, means, and the output's earlier readers
     const int etid = tid - 128, q = warp & 3, half = (warp - 4) >> 2;
     uint32_t n = 0;
     bool ok = true;
@@ -639,6 +653,33 @@ int resident_pairs(const void* kern, int smem, int threads) {
   return n;
 }
 
+// Launch with an optional cluster, beside the launch before where `dependent`.
+template <typename... P, typename... A>
+cudaError_t launch_beside(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem,
+                          unsigned cluster, bool dependent, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   CUtensorMap ta, tb;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
@@ -681,18 +722,7 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   const int rest = p.total - p.full;
   p.split = rest ? std::min(units / rest, p.maxch) : 1;
   if (p.full == 0) units = rest * p.split;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2u * (unsigned)units);
-  cfg.blockDim = dim3(NTHR);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+  e = launch_beside(kern, 2u * (unsigned)units, NTHR, SMEM, 2, w.dependent, s, ta, tb, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8");
 }
 
@@ -712,22 +742,25 @@ constexpr int RW = RT / 32;
 
 struct Line { uint32_t v[8]; };
 
-// 32 bytes, zeros past the end of the row or of the rows
+// 32 bytes, zeros past the end of the row or of the rows. All loads are volatile: weights are asked
+// for before dependency_wait() and codes after it, in the order written.
 __device__ __forceinline__ Line load32(const int8_t* p, bool in, bool wide) {
   Line l;
   if (!in) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) l.v[i] = 0u;
   } else if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(l.v[0]), "=r"(l.v[1]), "=r"(l.v[2]), "=r"(l.v[3]), "=r"(l.v[4]),
                    "=r"(l.v[5]), "=r"(l.v[6]), "=r"(l.v[7])
                  : "l"(p));
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-    l.v[0] = a.x; l.v[1] = a.y; l.v[2] = a.z; l.v[3] = a.w;
-    l.v[4] = b.x; l.v[5] = b.y; l.v[6] = b.z; l.v[7] = b.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(l.v[4 * h]), "=r"(l.v[4 * h + 1]), "=r"(l.v[4 * h + 2]),
+                     "=r"(l.v[4 * h + 3])
+                   : "l"(p + 16 * h));
   }
   return l;
 }
@@ -787,7 +820,8 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
   constexpr int NO = NT > 2 ? 2 : 1;
   const int oc = tid & 15;
   OutConst c0 = {};
-  if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
+  dependents_begin();
+  bool waited = false;
   int acc[NT][4] = {};
   for (int s0 = warp; s0 < segs; s0 += RW * RU) {
     Line wr[RU][2], x[RU][NT];
@@ -797,6 +831,11 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
       const bool in = k + 32 * i < p.K;   // N % 16 == 0: the channels are all there
       wr[u][0] = load32(w0 + k, in, rp.wide_w);
       wr[u][1] = load32(w1 + k, in, rp.wide_w);
+    }
+    if (!waited) {   // the first weights are on their way
+      dependency_wait();
+      waited = true;
+      if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
     }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
@@ -814,6 +853,10 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
         for (int j = 0; j < 8; j += 2)
           mma_s8(acc[n], wr[u][0].v[j], wr[u][1].v[j], wr[u][0].v[j + 1], wr[u][1].v[j + 1],
                  x[u][n].v[j], x[u][n].v[j + 1]);
+  }
+  if (!waited) {   // a warp without a segment
+    dependency_wait();
+    if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
   }
   // channels g and g + 8 of tokens 2 i and 2 i + 1
 #pragma unroll
@@ -836,7 +879,7 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
 }
 
 template <int NT>
-void launch_rows(const RowParams& p, cudaStream_t s) {
+cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
   // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
   // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
   // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
@@ -845,9 +888,8 @@ void launch_rows(const RowParams& p, cudaStream_t s) {
   const unsigned grid = (unsigned)(p.w.N / 16);
   constexpr int D = NT == 1 ? 2 : 1;
   if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)device_sms())
-    k_gemm_w8_rows<NT, 2 * D, 2><<<grid, RT, 0, s>>>(p);
-  else
-    k_gemm_w8_rows<NT, D, 3><<<grid, RT, 0, s>>>(p);
+    return launch_beside(k_gemm_w8_rows<NT, 2 * D, 2>, grid, RT, 0, 1, p.w.dependent, s, p);
+  return launch_beside(k_gemm_w8_rows<NT, D, 3>, grid, RT, 0, 1, p.w.dependent, s, p);
 }
 
 oq_status run_rows(const W8Params& w, cudaStream_t s) {
@@ -855,11 +897,10 @@ oq_status run_rows(const W8Params& w, cudaStream_t s) {
   p.w = w;
   p.wide_a = (reinterpret_cast<uintptr_t>(w.a) & 31u) == 0;
   p.wide_w = (reinterpret_cast<uintptr_t>(w.w) & 31u) == 0;
-  if (w.T <= 8) launch_rows<1>(p, s);
-  else if (w.T <= 16) launch_rows<2>(p, s);
-  else if (w.T <= 24) launch_rows<3>(p, s);
-  else launch_rows<4>(p, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = w.T <= 8    ? launch_rows<1>(p, s)
+                        : w.T <= 16 ? launch_rows<2>(p, s)
+                        : w.T <= 24 ? launch_rows<3>(p, s)
+                                    : launch_rows<4>(p, s);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_rows");
 }
 
@@ -886,10 +927,6 @@ struct SplitParams {
   int off_bar;                             // ring and partial sums lie in front of the barriers
 };
 
-__device__ __forceinline__ void dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(PT)
     k_gemm_w8_split(const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_a,
@@ -902,6 +939,7 @@ __global__ void __launch_bounds__(PT)
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kRingMax + 1);   // TMEM base, abort
   volatile uint32_t* s_abort = misc + 1;
   float2* s_tok = reinterpret_cast<float2*>(smem + sp.off_bar + 256);
+  dependents_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = (int)dev::cluster_nctarank(), r = (int)dev::cluster_ctarank();
   const int o0 = ((int)blockIdx.x / S) * PM;
@@ -1101,18 +1139,8 @@ oq_status run_split(const W8Params& w, cudaStream_t s) {
   const auto kern = &k_gemm_w8_split;
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8_split)");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * best));
-  cfg.blockDim = dim3(PT);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)best;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tw, ta, p);
+  e = launch_beside(kern, (unsigned)(tiles * best), PT, (size_t)smem, (unsigned)best, w.dependent, s,
+                    tw, ta, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_split");
 }
 
@@ -1128,7 +1156,7 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.a = g.a; p.w = g.w; p.a_scale = g.a_scale; p.mean = g.mean; p.w_scale = g.w_scale;
   p.w_rowsum = g.w_rowsum; p.bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
   p.T = (int)g.T; p.K = (int)g.K; p.N = (int)g.N; p.out_acc = g.out_acc;
-  p.n_head = (int)g.n_head; p.out = g.out; p.head = g.head;
+  p.n_head = (int)g.n_head; p.out = g.out; p.head = g.head; p.dependent = g.dependent;
   p.wide = (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");

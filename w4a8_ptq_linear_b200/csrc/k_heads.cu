@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "oq_internal.h"
 
@@ -34,6 +35,7 @@ struct HeadParams {
   int D, norm, rope, rot;
   int chunk_q, chunk_k;       // heads of a chunk
   int cq, ck;                 // chunks of a token
+  bool dependent;             // begin beside the launch before (float input)
   bool small;                 // items (tokens x chunks) within 31 bits
   float eps, inv_d;
   const float* cos;
@@ -161,8 +163,13 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
                        src + (int64_t)(h + u) * io.si[2]);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // Float input comes from a GEMM that this grid may begin beside: the factors, which do not, are
+  // made first. Else the elements are asked for first.
+  constexpr bool kAfter = std::is_same<TIN, float>::value;
+  if constexpr (!kAfter) {
 #pragma unroll
-  for (int st = 0; st < NS; ++st) fetch(st, h0 + st * U);
+    for (int st = 0; st < NS; ++st) fetch(st, h0 + st * U);
+  }
   // Element x of a pair whose other element is o becomes r (x A + o B) + C, r the norm's factor:
   // A = w c, B = -/+ w_o s, C = b c -/+ b_o s (o, w_o, b_o of the other element); A = w, B = 0,
   // C = b, o = 0 where nothing is turned, so that an infinity stays in its element.
@@ -213,6 +220,11 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
     }
   }
   const int mate = (threadIdx.x & 31) + (eo - e0) / 8;
+  if constexpr (kAfter) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+    for (int st = 0; st < NS; ++st) fetch(st, h0 + st * U);
+  }
 
   __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(io.out) + b * io.so[0] + s * io.so[1] + e0;
   int h = h0, st = 0;
@@ -285,8 +297,16 @@ oq_status run_u(HeadParams& p, int chunk, cudaStream_t s) {
   if (blocks > 0x7FFFFFFF)
     return fail(OQ_ERR_INVALID_ARG, "too many heads in one call: split the batch");
   p.small = items + HT < (int64_t)0x7FFFFFFF;
-  k_heads<TIN, G, U, NS><<<(unsigned)blocks, HT, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(HT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = std::is_same<TIN, float>::value && p.dependent ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_heads<TIN, G, U, NS>, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch heads");
 }
 
@@ -329,6 +349,7 @@ oq_status launch_heads(const HeadArgs& a, cudaStream_t s) {
   p.n_pos = a.n_pos;
   p.positions = a.positions;
   p.pos_bs = a.pos_batch_stride;
+  p.dependent = a.dependent;
   return a.in_f32 ? run_g<float>(p, s) : run_g<__nv_bfloat16>(p, s);
 }
 

@@ -468,10 +468,9 @@ oq_status oq_plan_get_codebook(const oq_plan* plan, int levels, double* centroid
   return OQ_OK;
 }
 
-static oq_status rotate_quantize_impl(const oq_plan* plan, const void* x, int64_t T, int64_t ldx,
-                                      void* codes, float* scale, float* mean, float* rotated,
-                                      float* rowsum, int mode, int center, int wlayout,
-                                      cudaStream_t s) {
+static RqArgs rotate_args(const oq_plan* plan, const void* x, int64_t T, int64_t ldx, void* codes,
+                          float* scale, float* mean, float* rotated, float* rowsum, int mode,
+                          int center, int wlayout) {
   RqArgs a;
   a.x = x; a.ldx = ldx; a.T = T; a.d = plan->d; a.h = plan->h; a.rounds = plan->rounds;
   a.center = center; a.mode = mode; a.tab = plan->d_tab; a.smask = plan->d_smask;
@@ -480,7 +479,15 @@ static oq_status rotate_quantize_impl(const oq_plan* plan, const void* x, int64_
   a.mean = mean; a.rotated = rotated; a.rowsum = rowsum; a.wlayout = wlayout;
   a.thr8 = plan->d_thr8;
   for (int i = 0; i < 15; ++i) a.thr[i] = (float)plan->cb_t[i];
-  return launch_rotate_quant(a, s);
+  return a;
+}
+
+static oq_status rotate_quantize_impl(const oq_plan* plan, const void* x, int64_t T, int64_t ldx,
+                                      void* codes, float* scale, float* mean, float* rotated,
+                                      float* rowsum, int mode, int center, int wlayout,
+                                      cudaStream_t s) {
+  return launch_rotate_quant(rotate_args(plan, x, T, ldx, codes, scale, mean, rotated, rowsum, mode,
+                                         center, wlayout), s);
 }
 
 oq_status oq_rotate_quantize(const oq_plan* plan, const void* x_bf16, int64_t T, int64_t ldx,
@@ -842,14 +849,25 @@ static oq_status linear_w8a8_impl(const oq_plan* plan, const void* x, int64_t T,
                                  plan->d, d_out, OQ_OUT_BF16,
                                  T == 0 && !y ? static_cast<const void*>(w) : y);
   if (st != OQ_OK) return st;
-  st = oq_rotate_quantize(plan, x, T, ldx, ws, scale, mean, nullptr, stream);
+  if (ldx < plan->d || (ldx * 2) % 16) return fail(OQ_ERR_MISALIGNED, "ldx must be >= d and a multiple of 8");
+  if (T > 0 && !x) return fail(OQ_ERR_INVALID_ARG, "NULL x");
+  if (!aligned16(x)) return fail(OQ_ERR_MISALIGNED, "x must be 16-byte aligned");
+  st = check_plan_device(plan);
+  if (st != OQ_OK) return st;
+  // the GEMM begins beside the two-token kernel (wider rows take the other kernel, one after one)
+  const bool beside = plan->d <= kRqPairMaxD;
+  const RqArgs rq = rotate_args(plan, x, T, ldx, ws, scale, plan->center ? mean : nullptr, nullptr,
+                                nullptr, kRqInt8, plan->center, 0);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = beside ? launch_rotate_quant_lead(rq, s) : launch_rotate_quant(rq, s);
   if (st != OQ_OK) return st;
   GemmW8Args g;
+  g.dependent = beside;
   g.a = reinterpret_cast<const int8_t*>(ws); g.a_scale = scale;
   g.mean = plan->center ? mean : nullptr;
   g.w = w; g.w_scale = w_scale; g.w_rowsum = w_rowsum; g.bias = bias; g.T = T; g.K = plan->d;
   g.N = d_out; g.out = y; g.head = head; g.n_head = n_head; g.heads = heads;
-  return launch_gemm_w8(g, static_cast<cudaStream_t>(stream));
+  return launch_gemm_w8(g, s);
 }
 
 // what oq_linear_w8a8 and oq_linear_qkv check of the layer before anything is launched
@@ -971,7 +989,7 @@ oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* 
   if (st != OQ_OK) return st;
   const int64_t ld = head ? n_head : d_out;
   const int esz = head ? 4 : 2;
-  a.in_f32 = head != nullptr;
+  a.in_f32 = a.dependent = head != nullptr;   // beside the INT8 GEMM
   const uint8_t* src = head ? reinterpret_cast<const uint8_t*>(head)
                             : static_cast<const uint8_t*>(y_bf16);
   a.q.in = src;

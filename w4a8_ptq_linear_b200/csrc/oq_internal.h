@@ -101,6 +101,9 @@ struct RqArgs {
   const float* thr8 = nullptr;  // kRqLloydMax8: 256 floats (255 thresholds + pad), device
 };
 oq_status launch_rotate_quant(const RqArgs& a, cudaStream_t s);
+// The same for kRqInt8 and d <= kRqPairMaxD, in a kernel that lets a dependent launch (dependent in
+// GemmW8Args) begin before it ends.
+oq_status launch_rotate_quant_lead(const RqArgs& a, cudaStream_t s);
 // Kernel-order gather table helpers: the row position thread t, register i gathers in a
 // round, where the staged input row keeps channel j, and where the fp32 round buffer keeps
 // rotated position p (the last two depend on which kernel shape width d uses).
@@ -169,6 +172,7 @@ struct HeadIo {                     // one of q, k
 struct HeadArgs {
   HeadIo q, k;
   int in_f32 = 0;
+  bool dependent = false;           // the launch before on the stream is a GEMM that writes `in` (float)
   int64_t batch = 0, seq = 0;
   int head_dim = 0, norm = 0, rope = 0, rot_dim = 0;
   float eps = 0.f;
@@ -197,6 +201,9 @@ struct GemmW8Args {
   float* head = nullptr;
   int64_t n_head = 0;
   const HeadArgs* heads = nullptr;
+  // The launch before on the stream is launch_rotate_quant_lead and writes a, a_scale and mean: the
+  // GEMM may begin beside it. Everything else that it reads was written earlier.
+  bool dependent = false;
 };
 oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s);
 // Whether the GEMM for T tokens can form these heads in its epilogue.
