@@ -557,11 +557,13 @@ def gemm_w8a8(a, a_scale, w_codes, w_scale, *, mean=None, w_rowsum=None, bias=No
     dt = torch.bfloat16 if out_kind == OUT_BF16 else torch.int32
     if out is None:
         out = a.new_empty((T, N), dtype=dt)
+    else:
+        _need(out, "out", dt, (T, N), dev)
     _check(lib().oq_gemm_w8a8(
         ap, _need(a_scale, "a_scale", f32, (T,), dev), _need_opt(mean, "mean", f32, (T,), dev), wp,
         _need(w_scale, "w_scale", f32, (N,), dev), _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev),
         _need_opt(bias, "bias", torch.bfloat16, (N,), dev), T, K, N, out_kind,
-        _need(out, "out", dt, (T, N), dev), _raw_stream(stream, dev)))
+        out.data_ptr(), _raw_stream(stream, dev)))
     return out
 
 
@@ -576,11 +578,13 @@ def linear_w8a8(plan: Plan, x, w_codes, w_scale, w_rowsum=None, bias=None, *, wo
         raise OQError(OQ_ERR_INVALID_ARG, f"w_codes: {Kw} columns, plan d={plan.d}")
     if out is None:
         out = x.new_empty((T, N))
+    else:
+        _need(out, "out", bf16, (T, N), dev)
     ws, nbytes, keep = _scratch(workspace, plan.workspace_bytes(T), x, stream)
     _check(lib().oq_linear_w8a8(
         plan.handle, xp, T, ldx, wp, _need(w_scale, "w_scale", f32, (N,), dev),
         _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev), _need_opt(bias, "bias", bf16, (N,), dev),
-        N, _need(out, "out", bf16, (T, N), dev), ws, nbytes, _raw_stream(stream, dev)))
+        N, out.data_ptr(), ws, nbytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -713,14 +717,16 @@ def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None
     pos, pbs = _positions(positions, batch, S, dev)
     if out is None:
         out = x.new_empty((T, N))
+    else:
+        _need(out, "out", bf16, (T, N), dev)
     L, kind = lib(), W_INT8 if w8 else W_INT4
     need = L.oq_linear_qkv_workspace_bytes(plan.handle, heads._ref, kind, T, N)
     ws, nbytes, keep = _scratch(workspace, need, x, stream)
     _check(L.oq_linear_qkv(
         plan.handle, heads._ref, xp, batch, S, ldx, kind, wp,
         _need(w_scale, "w_scale", f32, (N,), dev), _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev),
-        _need_opt(bias, "bias", bf16, (N,), dev), N, pos, pbs, _need(out, "out", bf16, (T, N), dev),
-        ws, nbytes, _raw_stream(stream, dev)))
+        _need_opt(bias, "bias", bf16, (N,), dev), N, pos, pbs, out.data_ptr(), ws,
+        nbytes, _raw_stream(stream, dev)))
     return out
 
 
