@@ -12,7 +12,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include "oq_internal.h"
 #include "ptx.cuh"
@@ -624,23 +624,23 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
 }
 
-// CTA pairs that are resident at once, per kernel and device (0 if the query fails).
-int resident_pairs(const void* kern, int smem, int threads) {
+// Clusters that are resident at once, per device and launch shape (0 if the query fails).
+int resident_clusters(const void* kern, int cluster, int smem, int threads) {
   static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> kept;
-  int dev = 0, sms = 0;
+  static std::map<std::tuple<int, const void*, int, int>, int> kept;
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  auto found = kept.find({kern, dev});
+  const auto key = std::make_tuple(dev, kern, cluster, smem);
+  auto found = kept.find(key);
   if (found != kept.end()) return found->second;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2u * (unsigned)std::max(sms, 1));
+  cfg.gridDim = dim3((unsigned)(cluster * device_sms()));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -649,7 +649,7 @@ int resident_pairs(const void* kern, int smem, int threads) {
     cudaGetLastError();
     n = 0;
   }
-  kept[{kern, dev}] = n;
+  kept[key] = n;
   return n;
 }
 
@@ -691,7 +691,7 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   const auto kern = heads ? &k_gemm_w8<true> : &k_gemm_w8<false>;
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8)");
-  int units = resident_pairs(reinterpret_cast<const void*>(kern), SMEM, NTHR);
+  int units = resident_clusters(reinterpret_cast<const void*>(kern), 2, SMEM, NTHR);
   if (units <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no CTA pair fits on this device");
   TileParams p{};
   p.w = w;
@@ -1102,33 +1102,64 @@ __global__ void __launch_bounds__(PT)
   }
 }
 
-oq_status run_split(const W8Params& w, cudaStream_t s) {
+// How a product is split, and what it is expected to take (see choose_shape).
+struct SplitPlan {
+  int S = 0, ks = 0, ns = 0, off_bar = 0, smem = 0;
+  double us = 1e30;
+};
+
+SplitPlan plan_split(const W8Params& w) {
+  const int npad = (w.T + 15) / 16 * 16, nkb = (w.K + 127) / 128, tiles = (w.N + PM - 1) / PM;
+  const void* kern = reinterpret_cast<const void*>(&k_gemm_w8_split);
+  static std::mutex mu;
+  static std::map<std::tuple<int, int, int, int>, SplitPlan> kept;
+  SplitPlan best;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || allow_max_dynamic_smem(kern) != cudaSuccess) return best;
+  const auto key = std::make_tuple(dev, npad, nkb, tiles);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    auto found = kept.find(key);
+    if (found != kept.end()) return found->second;
+  }
+  const double sms = device_sms();
+  for (int S = 1; S <= kSplitMax; ++S) {
+    SplitPlan c;
+    c.S = S;
+    c.ks = (nkb + S - 1) / S;
+    if ((S - 1) * c.ks >= nkb) continue;   // a CTA would have nothing to do
+    // ring: as deep as the CTA has blocks, within half an SM's shared memory where the partial sums
+    // leave room for two CTAs, else within all of it; at least as large as the partial sums
+    const int stage = PWB + npad * 128;
+    const int room = npad <= 192 ? 108 * 1024 : 216 * 1024;
+    c.ns = std::min(std::min(c.ks, kRingMax), room / stage);
+    c.off_bar = (std::max(c.ns * stage, npad * PM * 4) + 1023) / 1024 * 1024;
+    c.smem = c.off_bar + 256 + 8 * kSplitTokens + 1024;
+    const int fit = resident_clusters(kern, S, c.smem, PT);
+    if (fit <= 0) continue;
+    // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
+    // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters that
+    // does not fit waits for the one before)
+    const int waves = (tiles + fit - 1) / fit;
+    const double share = std::max(1.0, std::min(tiles, fit) * S / sms);
+    c.us = waves * (5.6 + 0.02 * npad + share * c.ks * (0.36 + 0.0004 * npad) + 0.2 * S);
+    if (c.us < best.us) best = c;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  kept[key] = best;
+  return best;
+}
+
+oq_status run_split(const W8Params& w, const SplitPlan& plan, cudaStream_t s) {
   SplitParams p{};
   p.w = w;
   p.npad = (w.T + 15) / 16 * 16;
   p.tcols = 32;
   while (p.tcols < p.npad) p.tcols *= 2;
   p.nkb = (w.K + 127) / 128;
-  const int tiles = (w.N + PM - 1) / PM, sms = device_sms();
-  // The split that leaves the fullest SM the fewest K blocks; of equal ones the smallest. A further
-  // CTA in the cluster costs about as much as a sixteenth of a K block's time in barriers.
-  int best = 1, ks = p.nkb;
-  int64_t cost = INT64_MAX;
-  for (int S = 1; S <= kSplitMax; ++S) {
-    const int k = (p.nkb + S - 1) / S;
-    if ((S - 1) * k >= p.nkb) continue;   // a CTA would have nothing to do
-    const int64_t c = 16 * (((int64_t)tiles * S + sms - 1) / sms) * k + S;
-    if (c < cost) cost = c, best = S, ks = k;
-  }
-  p.ks = ks;
-  // ring: as deep as the CTA has blocks, within half an SM's shared memory where the tokens are few
-  // (two CTAs to an SM), else within all of it; at least as large as the partial sums
-  const int stage = PWB + p.npad * 128;
-  const int room = p.npad <= 64 ? 108 * 1024 : 216 * 1024;
-  p.ns = std::min(std::min(ks, kRingMax), room / stage);
-  const int ring = std::max(p.ns * stage, p.npad * PM * 4);
-  p.off_bar = (ring + 1023) / 1024 * 1024;
-  const int smem = p.off_bar + 256 + 8 * kSplitTokens + 1024;
+  p.ks = plan.ks;
+  p.ns = plan.ns;
+  p.off_bar = plan.off_bar;
   CUtensorMap tw, ta;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
   if (!tma_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, PM,
@@ -1136,12 +1167,28 @@ oq_status run_split(const W8Params& w, cudaStream_t s) {
       !tma_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.a, K, T, K, 128, (uint32_t)p.npad,
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return fail(OQ_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable");
-  const auto kern = &k_gemm_w8_split;
-  cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8_split)");
-  e = launch_beside(kern, (unsigned)(tiles * best), PT, (size_t)smem, (unsigned)best, w.dependent, s,
-                    tw, ta, p);
+  const int tiles = (w.N + PM - 1) / PM;
+  const cudaError_t e = launch_beside(k_gemm_w8_split, (unsigned)(tiles * plan.S), PT,
+                                      (size_t)plan.smem, (unsigned)plan.S, w.dependent, s, tw, ta, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_split");
+}
+
+// ---- which shape -------------------------------------------------------------------------------
+// All three give the same bits, so the choice is one of time alone, by estimates (us) fitted to
+// measurements on this device. Rows: the weights at the HBM rate, and the tokens once for every 16
+// channels at the L2 rate. Tiles: 128 bytes of K of a tile, by its width. Measured against
+// estimate: rows 1 x 4096 x 4096 5.1 (5.1), 32 x 4096 x 12288 18.4 (18.0); split 40 x 4096 x 4096
+// 9.6 (9.7), 128 x 4096 x 12288 18.6 (17.2), 256 x 12288 x 4096 21.7 (22.6); tiles 256 x 4096 x 12288 21.0
+// (21.2), 256 x 4096 x 4096 14.8 (15.0).
+double rows_us(const W8Params& w) {
+  const double bytes = (double)w.N * w.K;
+  return 2.2 + bytes / 6.2e6 + bytes * w.T / 16 / 13e6;
+}
+double tiles_us(const W8Params& w) {
+  const int npm = (w.N + CH - 1) / CH, ncol = (npm * CH + TN - 1) / TN;   // T <= 256: one token block
+  const int units = std::max(device_sms() / 2, 1);
+  const int split = std::max(1, std::min(units / ncol, TN / CH)), waves = (ncol + units - 1) / units;
+  return 6.8 + waves * ((w.K + 127) / 128) * (0.19 + 0.00102 * TN / split);
 }
 
 }  // namespace
@@ -1161,9 +1208,12 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");
   p.limit_ns = kWaitLimitNs;
-  if (g.T <= kRowTokens) return run_rows(p, s);
-  if (g.T <= kSplitTokens) return run_split(p, s);
-  return run_tiles(p, g.heads, s);
+  // heads come with tiles only (gemm_w8_forms_heads)
+  if (g.T > kSplitTokens || g.heads) return run_tiles(p, g.heads, s);
+  const SplitPlan split = plan_split(p);
+  if (g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, s);
+  if (split.S > 0 && split.us <= tiles_us(p)) return run_split(p, split, s);
+  return run_tiles(p, nullptr, s);
 }
 
 }  // namespace oq
