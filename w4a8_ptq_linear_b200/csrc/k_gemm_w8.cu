@@ -1135,8 +1135,12 @@ SplitPlan plan_split(const W8Params& w) {
     c.ns = std::min(std::min(c.ks, kRingMax), room / stage);
     c.off_bar = (std::max(c.ns * stage, npad * PM * 4) + 1023) / 1024 * 1024;
     c.smem = c.off_bar + 256 + 8 * kSplitTokens + 1024;
-    const int fit = resident_clusters(kern, S, c.smem, PT);
-    if (fit <= 0) continue;
+    if (resident_clusters(kern, S, c.smem, PT) <= 0) continue;   // does not launch here
+    // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
+    // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
+    // occupancy query counts one CTA to an SM; 192 CTAs in pairs ran faster than 96 alone).
+    const double slots = (c.smem <= 112 * 1024 ? 2 : 1) * sms;
+    const int fit = std::max(1, (int)(S == 1 ? slots : 0.9 * slots / S));
     // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
     // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters that
     // does not fit waits for the one before)
