@@ -53,7 +53,8 @@ __device__ __forceinline__ void dependents_begin() {
 }
 
 // A walk over the stages of a ring. One thread issues a role's steps, so its own instructions are on
-// the critical path: a division for the stage and the phase of each step took 0.1 us of it.
+// the critical path: without a division for the stage and the phase of each step the few-token product
+// took 8.3 us instead of 8.8 (16 x 4096 x 4096).
 struct Ring {
   int st = 0;
   uint32_t phase = 0;
@@ -82,17 +83,23 @@ __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatil
 // sums over a row stay in the thread.
 //
 // One persistent CTA pair per two SMs. Both operands come by TMA, K-major, 128 bytes of K to a
-// block; two producer threads, one to an operand (one thread's TMA reads from L2 run at about
-// 32 bytes a clock, a full tile needs 64 per CTA). TMEM holds two accumulators of 256 columns, so a
-// tile's epilogue runs under the next tile's MMAs.
+// block; two producer threads, one to an operand. TMEM holds two accumulators of 256 columns, so a
+// tile's epilogue runs under the next tile's MMAs; it writes 32-byte sectors from registers.
 //
-// What bounds it: a 256 x 256 tile reads 64 KB per 128 bytes of K for 2 * 256 * 256 * 128 operations,
-// 64 bytes a clock and SM at the tensor pipe's full rate, which is about what L2 delivers.
+// What bounds it is L2 and shared memory together. A full tile brings 64 KB per 128 bytes of K
+// through L2, writes them to shared memory and reads them again for the MMAs: at the tensor pipe's
+// full rate 64 bytes a clock and SM from L2 and all 128 of shared memory. Measured at 4096 x 4096 x
+// 12288, parts left out in a copy of the kernel: MMAs alone 102 us (4.05 POPS), loads alone 127,
+// both 132, with the epilogue's arithmetic 139, whole 142 us (2.9 POPS, 68 % of the kind::i8 peak
+// loop of 4.3; a library product of the same operands to int32 takes 137 to 141). Under the power cap of
+// a long run 160 to 170 us (the library 158). Hence stages of two K blocks (one commit for eight
+// MMAs; of one block 167 us where two took 155), no staging of the output in shared memory, constants
+// read from it only where they count.
 //
 // Schedule: tiles in waves, one to a pair, down the token blocks of a group first, so that the
-// tiles in flight share their weights and the group's activations stay in L2 (ranges of tiles
-// contiguous in a token block kept all weights live at once and took 154 us instead of XX at 4096 x
-// 4096 x 12288). What does not fill a wave is cut into narrower tiles, one to a pair.
+// tiles in flight share their weights and the group's activations stay in L2 (contiguous ranges of
+// tiles for each pair kept all weights live at once: 154 us where waves took 146). What does not
+// fill a wave is cut into narrower tiles, one to a pair.
 constexpr int TM = 128;                    // tokens per CTA
 constexpr int TN = 256;                    // channels per tile at most
 constexpr int CH = 64;                     // channels per chunk, where no heads are formed
@@ -183,7 +190,7 @@ __device__ __forceinline__ uint32_t pack2(float2 y) {
 }
 
 // y of a token's NF neighbouring channels: c = fma(mean, w1, b), y = fma(acc, alpha s, c). The
-// channels' constants lie at cs (scales), cs + TN (row sums) and cs + 2 TN (biases) floats, the last
+// channels' constants lie at col (scales), col + TN (row sums) and col + 2 TN (biases), the last
 // two read only where they count: shared memory is what the mainloop is short of.
 template <int NF>
 __device__ __forceinline__ void dequant(const uint32_t (&r)[NF], float alpha, float mean,
@@ -256,6 +263,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   };
 #pragma unroll 1
   for (int c = 0; c < h.D; c += 32) {
+    __syncwarp();
     dev::tmem_ld32(acc + (uint32_t)c, v);
     dev::tmem_wait_ld();
     dequant<32>(v, alpha, mean, col + c, p.mean != nullptr, p.bias != nullptr, y);
@@ -303,6 +311,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   if (h.rope == OQ_ROPE_HALVES) {
 #pragma unroll 1
     for (int i = 0; i < half; i += 16) {
+      __syncwarp();   // the lanes' ways part below; TMEM is read by the whole warp
       uint32_t a[16], d[16];
       dev::tmem_ld16(acc + (uint32_t)i, a);
       dev::tmem_ld16(acc + (uint32_t)(i + half), d);
@@ -335,6 +344,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   } else {
 #pragma unroll 1
     for (int c = 0; c < h.rot; c += 32) {
+      __syncwarp();
       dev::tmem_ld32(acc + (uint32_t)c, v);
       dev::tmem_wait_ld();
 #pragma unroll
@@ -359,6 +369,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   }
 #pragma unroll 1
   for (int c = h.rot; c < h.D; c += 32) {   // elements that no rotation reaches
+    __syncwarp();
     dev::tmem_ld32(acc + (uint32_t)c, v);
     dev::tmem_wait_ld();
 #pragma unroll
@@ -451,6 +462,9 @@ __global__ void __launch_bounds__(NTHR, 1)
         const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * cw + (int)rank * rows;
         for (int st = 0; st < nst; ++st, ++j, rg.next(SK)) {
           const int s = rg.st, nk = min(KS, nkb - st * KS);
+          // the ring is full of weights: the limit of a wait does not run while the tokens are
+          // still being made
+          if (!tok && j == (uint32_t)SK) dependency_wait();
           if (!ring_wait(free_bar(s), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) {
             ok = false;
             break;
@@ -481,6 +495,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (the leader's lane 0) ----------------
     if (lane == 0 && rank == 0) {
+      dependency_wait();
       const uint64_t da = dev::sdesc_sw128(dev::smem_u32(smem));
       const uint64_t db = dev::sdesc_sw128(dev::smem_u32(smem) + OFF_B);
       uint32_t n = 0;
@@ -581,10 +596,11 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll 1
         for (int c = first; ok && c < last; c += step) {
           uint32_t r[32];
+          __syncwarp();   // lanes of missing tokens have gone ahead; TMEM is read by the whole warp
           dev::tmem_ld32(acc + (uint32_t)(c * 32), r);
           dev::tmem_wait_ld();
           const int o = o0 + c * 32;
-          if (t >= p.T || o >= p.N) continue;   // no warp-wide step below
+          if (t >= p.T || o >= p.N) continue;
           const bool two = o + 16 < p.N;        // N % 16 == 0: sixteen or all of the channels
           if (!HEADS && p.out_acc) {
             int32_t* dst = reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o;
@@ -728,7 +744,8 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 
 // ---- few tokens ------------------------------------------------------------------------------
 // Up to 32 tokens: bound by the weights' bytes (4096 x 4096: 16.8 MB, 2.6 us of HBM) and by latency, so
-// nothing is staged. A block takes 16 channels and all of K: its eight warps read the weight rows
+// nothing is staged (one token 5.1 us, 4096 x 12288 10.3 us or 4.9 TB/s, with every call's weights from HBM;
+// tiles 19.9 us). A block takes 16 channels and all of K: its eight warps read the weight rows
 // straight into registers, all loads of a warp in flight together, and feed mma.sync (m16n8k32,
 // weights as the 16 rows, tokens as the 8 columns); their sums meet in shared memory.
 //
@@ -980,6 +997,7 @@ __global__ void __launch_bounds__(PT)
       const int row = warp == 0 ? o0 : 0;
       Ring rg;
       for (int k = 0; k < nk; ++k, rg.next(ns)) {
+        if (k == ns) dependency_wait();   // the limit of a wait starts with the tokens
         if (k >= ns && !ring_wait(free_bar(rg.st), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) break;
         dev::mbar_arrive_expect_tx(full(rg.st), bytes);
         dev::tma_load_2d(first + (uint32_t)(rg.st * stage), map, (kb0 + k) * 128, row, full(rg.st));
@@ -989,6 +1007,7 @@ __global__ void __launch_bounds__(PT)
     __syncwarp();
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer ----------------
+    dependency_wait();
     const uint32_t idesc = dev::idesc_i8(PM, sp.npad);
     const uint64_t dw = dev::sdesc_sw128(dev::smem_u32(smem));
     const uint64_t dx = dev::sdesc_sw128(dev::smem_u32(smem) + PWB);
