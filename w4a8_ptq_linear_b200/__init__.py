@@ -518,6 +518,15 @@ def _need_2d(t, name, dtype, dev):
     return t.data_ptr(), *t.shape
 
 
+def _layer_bytes(plan, T):
+    """plan.workspace_bytes(T), asked of the library once for each T."""
+    kept = plan.__dict__.setdefault("_layer_bytes", {})
+    need = kept.get(T)
+    if need is None:
+        need = kept[T] = plan.workspace_bytes(T)
+    return need
+
+
 def _scratch(workspace, need, like, stream):
     """Pointer and size of the caller's workspace, or of one from torch's allocator that stays
     in use on `stream`; the tensor itself, to be kept until the call has been made."""
@@ -580,7 +589,7 @@ def linear_w8a8(plan: Plan, x, w_codes, w_scale, w_rowsum=None, bias=None, *, wo
         out = x.new_empty((T, N))
     else:
         _need(out, "out", bf16, (T, N), dev)
-    ws, nbytes, keep = _scratch(workspace, plan.workspace_bytes(T), x, stream)
+    ws, nbytes, keep = _scratch(workspace, _layer_bytes(plan, T), x, stream)
     _check(lib().oq_linear_w8a8(
         plan.handle, xp, T, ldx, wp, _need(w_scale, "w_scale", f32, (N,), dev),
         _need_opt(w_rowsum, "w_rowsum", f32, (N,), dev), _need_opt(bias, "bias", bf16, (N,), dev),

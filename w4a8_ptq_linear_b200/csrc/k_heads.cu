@@ -119,7 +119,7 @@ struct Raw<float> {
 
 // A chunk of one token's heads to a group, U at a time: the factors are made once for them, and a
 // round's loads are in flight while the round before is computed.
-template <typename TIN, int G, int U, int NS>
+template <typename TIN, int G, int U, int NS, bool HALVES>
 __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
   constexpr int SB = Raw<TIN>::kBytes;
   __shared__ __align__(16) uint8_t s_slot[NS][U][HT][SB];
@@ -153,14 +153,22 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
   if (p.positions) pos = p.positions[b * p.pos_bs + s];
   const int rounds = __reduce_max_sync(0xffffffffu, (h1 - h0 + U - 1) / U);   // of the warp
 
-  const TIN* src = reinterpret_cast<const TIN*>(io.in) + b * io.si[0] + s * io.si[1] + e0;
+  const TIN* src = reinterpret_cast<const TIN*>(io.in) + b * io.si[0] + s * io.si[1] +
+                   (int64_t)h0 * io.si[2] + e0;   // of the next heads to fetch
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(s_slot[0][0][threadIdx.x]);
+  if (!on) {   // lanes past the head: zeros that no load replaces (they enter the group's sums)
+#pragma unroll
+    for (int i = 0; i < NS * U * SB / 16; ++i)
+      *reinterpret_cast<uint4*>(&s_slot[i / (U * SB / 16)][i / (SB / 16) % U][threadIdx.x][16 * (i % (SB / 16))]) =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
   // U heads into stage st; an empty group where there are none, so that the groups can be counted
   auto fetch = [&](int st, int h) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (on && h + u < h1)
-        Raw<TIN>::send((uint32_t)__cvta_generic_to_shared(s_slot[st][u][threadIdx.x]),
-                       src + (int64_t)(h + u) * io.si[2]);
+        Raw<TIN>::send(slot0 + (uint32_t)((st * U + u) * HT * SB), src + u * io.si[2]);
+    src += U * io.si[2];
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // Float input comes from a GEMM that this grid may begin beside: the factors, which do not, are
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
   // C = b, o = 0 where nothing is turned, so that an infinity stays in its element.
   float2 A[4], B[4], C[4];
   const int half = p.rot / 2;
-  const bool pairs = p.rope == OQ_ROPE_PAIRS;
+  constexpr bool pairs = !HALVES;   // or nothing is turned
   bool turn = false;   // this lane's elements are turned
   int eo = e0;         // where the other elements lie (halves)
   {
@@ -226,22 +234,19 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
     for (int st = 0; st < NS; ++st) fetch(st, h0 + st * U);
   }
 
-  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(io.out) + b * io.so[0] + s * io.so[1] + e0;
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(io.out) + b * io.so[0] + s * io.so[1] +
+                       (int64_t)h0 * io.so[2] + e0;
   int h = h0, st = 0;
   for (int i = 0; i < rounds; ++i, h += U) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");   // this stage's has landed
     Raw<TIN> cur[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      cur[u].take(s_slot[st][u][threadIdx.x]);
-      // lanes and heads past the end: zeros (their sums enter the group's)
-      if (!(on && h + u < h1)) cur[u] = Raw<TIN>{};
-    }
+    for (int u = 0; u < U; ++u) cur[u].take(s_slot[st][u][threadIdx.x]);   // past the last head: unused
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float2 x[4], o[4];
       cur[u].get(x);
-      if (p.rope == OQ_ROPE_HALVES) {
+      if constexpr (HALVES) {
         cur[u].get_from(mate, turn, o);
       } else {
 #pragma unroll
@@ -277,15 +282,16 @@ __global__ void __launch_bounds__(HT, HB) k_heads(const HeadParams p) {
         out[j] = *reinterpret_cast<const uint32_t*>(&v);
       }
       if (on && h + u < h1)
-        *reinterpret_cast<uint4*>(dst + (int64_t)(h + u) * io.so[2]) =
+        *reinterpret_cast<uint4*>(dst + u * io.so[2]) =
             make_uint4(out[0], out[1], out[2], out[3]);
     }
+    dst += U * io.so[2];
     fetch(st, h + NS * U);   // this thread has read its slots
     st = st + 1 == NS ? 0 : st + 1;
   }
 }
 
-template <typename TIN, int G, int U, int NS>
+template <typename TIN, int G, int U, int NS, bool HALVES>
 oq_status run_u(HeadParams& p, int chunk, cudaStream_t s) {
   auto cut = [&](int heads, int& chunks, int& size) {   // into chunks of about the same size
     chunks = (heads + chunk - 1) / chunk;
@@ -306,27 +312,32 @@ oq_status run_u(HeadParams& p, int chunk, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = std::is_same<TIN, float>::value && p.dependent ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_heads<TIN, G, U, NS>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_heads<TIN, G, U, NS, HALVES>, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch heads");
 }
 
-template <typename TIN, int G>
+template <typename TIN, int G, bool HALVES>
 oq_status run(HeadParams& p, cudaStream_t s) {
   // Chunks as long as leaves two to every group the device holds at once, 32 heads at most: longer
   // ones make the factors less often, shorter ones fill the device. Below a head to a group, one
   // head each. Measured, heads of 128: 2 x 8192 tokens x 40 heads 62 us in chunks of 32, 73 in
   // chunks of 8; 128 tokens 3.6 us in chunks of 1, 4.7 in chunks of 8.
   const int64_t heads = p.tokens * (p.q.heads + p.k.heads), groups = (int64_t)device_sms() * HB * HT / G;
-  if (heads <= groups) return run_u<TIN, G, 1, 1>(p, 1, s);
-  return run_u<TIN, G, 2, 3>(p, (int)std::min<int64_t>(2 * heads / groups, 32), s);
+  if (heads <= groups) return run_u<TIN, G, 1, 1, HALVES>(p, 1, s);
+  return run_u<TIN, G, 2, 3, HALVES>(p, (int)std::min<int64_t>(2 * heads / groups, 32), s);
+}
+
+template <typename TIN, int G>
+oq_status run_rope(HeadParams& p, cudaStream_t s) {
+  return p.rope == OQ_ROPE_HALVES ? run<TIN, G, true>(p, s) : run<TIN, G, false>(p, s);
 }
 
 template <typename TIN>
 oq_status run_g(HeadParams& p, cudaStream_t s) {
-  if (p.D <= 32) return run<TIN, 4>(p, s);
-  if (p.D <= 64) return run<TIN, 8>(p, s);
-  if (p.D <= 128) return run<TIN, 16>(p, s);
-  return run<TIN, 32>(p, s);
+  if (p.D <= 32) return run_rope<TIN, 4>(p, s);
+  if (p.D <= 64) return run_rope<TIN, 8>(p, s);
+  if (p.D <= 128) return run_rope<TIN, 16>(p, s);
+  return run_rope<TIN, 32>(p, s);
 }
 
 }  // namespace
