@@ -10,11 +10,12 @@
 // into three factors per element, once for the heads of a group. Everything is float32, rounded to
 // bf16 once.
 //
-// Bound by HBM: 2 x 8192 tokens x (32 + 8) heads of 128, 344 MB, take 62 us (5.5 TB/s, 85 % of the
-// measured copy rate). What that needs is bytes in flight: the elements come by cp.async into
-// slots of shared memory that only their own thread reads (three stages of two heads to a group, no
-// registers held), and the factors are made once for up to 32 heads; a head to a group with
-// everything in registers took 157 us, four heads 93 us.
+// Bound by HBM: 2 x 8192 tokens x (32 + 8) heads of 128, 344 MB, take 57 us (6.0 TB/s, 91 % of the
+// measured copy rate; 4096 x 60 heads of 64: 13.8 us). What that needs is bytes in flight and few
+// instructions: the elements come by cp.async into slots of shared memory that only their own
+// thread reads (three stages of two heads to a group, no registers held), the factors are made once
+// for up to 32 heads, and the pairing is a template parameter. A head to a group with everything in
+// registers took 157 us, four heads 93, the slots 65, the pairing as a branch 61.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -26,7 +27,7 @@ namespace oq {
 namespace {
 
 constexpr int HT = 128;   // threads
-constexpr int HB = 6;     // blocks to an SM
+constexpr int HB = 7;     // blocks to an SM
 
 struct HeadParams {
   HeadIo q, k;
