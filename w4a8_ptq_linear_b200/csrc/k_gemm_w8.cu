@@ -58,6 +58,7 @@ __device__ __forceinline__ void dependents_begin() {
 struct Ring {
   int st = 0;
   uint32_t phase = 0;
+  bool alone = false;   // the launch before has ended
   __device__ __forceinline__ void next(int n) {
     if (++st == n) {
       st = 0;
@@ -67,10 +68,16 @@ struct Ring {
 };
 
 // Wait for a stage's barrier; false (and the CTA's abort flag set) when the wait gave up or another
-// role has. The flag is looked at only where the stage was not ready.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
-                                          const W8Params& p, uint32_t site) {
+// role has. The flag is looked at only where the stage was not ready, and the limit starts only when
+// the launch before has ended, for whose tokens the stage may be waiting.
+__device__ __forceinline__ bool ring_wait(Ring& rg, uint32_t bar, uint32_t parity,
+                                          volatile uint32_t* abort, const W8Params& p,
+                                          uint32_t site) {
   if (dev::mbar_try_wait(bar, parity)) return true;
+  if (!rg.alone) {
+    dependency_wait();
+    rg.alone = true;
+  }
   if (*abort == 0u && dev::mbar_wait(bar, parity, p.err, site, p.limit_ns)) return true;
   *abort = 1u;
   return false;
@@ -462,10 +469,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         const int row0 = tok ? (2 * m + (int)rank) * TM : c0 * cw + (int)rank * rows;
         for (int st = 0; st < nst; ++st, ++j, rg.next(SK)) {
           const int s = rg.st, nk = min(KS, nkb - st * KS);
-          // the ring is full of weights: the limit of a wait does not run while the tokens are
-          // still being made
-          if (!tok && j == (uint32_t)SK) dependency_wait();
-          if (!ring_wait(free_bar(s), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) {
+          if (!ring_wait(rg, free_bar(s), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) {
             ok = false;
             break;
           }
@@ -495,7 +499,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (the leader's lane 0) ----------------
     if (lane == 0 && rank == 0) {
-      dependency_wait();
       const uint64_t da = dev::sdesc_sw128(dev::smem_u32(smem));
       const uint64_t db = dev::sdesc_sw128(dev::smem_u32(smem) + OFF_B);
       uint32_t n = 0;
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       for (; ok && it.next(m, c0, nch); ++n) {
         const uint32_t idesc = dev::idesc_i8(2 * TM, nch * cw);
         const int b = n & 1;
-        if (!ring_wait(tempty_bar(b), ((n >> 1) & 1u) ^ 1u, s_abort, p, kSiteGemmAccum)) {
+        if (!ring_wait(rg, tempty_bar(b), ((n >> 1) & 1u) ^ 1u, s_abort, p, kSiteGemmAccum)) {
           ok = false;
           break;
         }
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         const uint32_t dt = tmem + (uint32_t)(b * TN);
         for (int st = 0; st < nst; ++st, rg.next(SK)) {
           const int s = rg.st, nk = min(KS, nkb - st * KS);
-          if (!ring_wait(full_bar(s), rg.phase, s_abort, p, kSiteGemmFull)) {
+          if (!ring_wait(rg, full_bar(s), rg.phase, s_abort, p, kSiteGemmFull)) {
             ok = false;
             break;
           }
@@ -997,8 +1000,7 @@ __global__ void __launch_bounds__(PT)
       const int row = warp == 0 ? o0 : 0;
       Ring rg;
       for (int k = 0; k < nk; ++k, rg.next(ns)) {
-        if (k == ns) dependency_wait();   // the limit of a wait starts with the tokens
-        if (k >= ns && !ring_wait(free_bar(rg.st), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) break;
+        if (k >= ns && !ring_wait(rg, free_bar(rg.st), rg.phase ^ 1u, s_abort, p, kSiteGemmEmpty)) break;
         dev::mbar_arrive_expect_tx(full(rg.st), bytes);
         dev::tma_load_2d(first + (uint32_t)(rg.st * stage), map, (kb0 + k) * 128, row, full(rg.st));
         issued = k + 1;
@@ -1007,13 +1009,12 @@ __global__ void __launch_bounds__(PT)
     __syncwarp();
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer ----------------
-    dependency_wait();
     const uint32_t idesc = dev::idesc_i8(PM, sp.npad);
     const uint64_t dw = dev::sdesc_sw128(dev::smem_u32(smem));
     const uint64_t dx = dev::sdesc_sw128(dev::smem_u32(smem) + PWB);
     Ring rg;
     for (int k = 0; k < nk; ++k, rg.next(ns)) {
-      if (!ring_wait(full(rg.st), rg.phase, s_abort, p, kSiteGemmFull)) break;
+      if (!ring_wait(rg, full(rg.st), rg.phase, s_abort, p, kSiteGemmFull)) break;
       dev::tc_fence_after();
       const uint64_t at = (uint64_t)((uint32_t)(rg.st * stage) >> 4);   // of the stage, 16-byte units
 #pragma unroll
