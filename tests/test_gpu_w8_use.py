@@ -129,6 +129,23 @@ def test_heads_outside_the_epilogue(D, rot, rope, norm, T):
     plan.close()
 
 
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_rows_wider_than_the_two_token_kernel(T):
+    # d > 8192: another rotate-quantize kernel, after which the GEMM does not begin early
+    oq = _oq()
+    d, N = 9216, 144
+    plan = oq.Plan(d, 1024, 1, seed=1, center=True)
+    x = to_torch_bf16(synth.make_x(T, d, mean_var=3.0, heavy_frac=0.0, seed=T))
+    codes, s, w1 = oq.prepare_weights_w8(plan, to_torch_bf16(synth.make_w(N, d)))
+    y = oq.linear_w8a8(plan, x, codes, s, w1)
+    a, sa, mean, _ = oq.rotate_quantize(plan, x)
+    assert torch.equal(y, oq.gemm_w8a8(a, sa, codes, s, mean=mean, w_rowsum=w1))
+    acc = a.double() @ codes.double().T
+    assert torch.equal(oq.gemm_w8a8(a, sa, codes, s, out_kind=oq.OUT_ACC).double(), acc)
+    _ok(oq)
+    plan.close()
+
+
 def test_many_tokens_of_one_small_head():
     oq = _oq()
     cos, sin = _tables(16, 16)
