@@ -146,6 +146,43 @@ def test_rows_wider_than_the_two_token_kernel(T):
     plan.close()
 
 
+@pytest.mark.parametrize("T", [2, 9, 13, 16, 17, 33, 257, 400])
+@pytest.mark.parametrize("D,rope,norm", [(64, "halves", "rms"), (128, "pairs", "layer"),
+                                         (96, "halves", "none")])
+def test_projection_around_its_shapes(T, D, rope, norm):
+    # whole and missing positions, weights and biases, on both sides of every change of shape; the
+    # two separate calls round the projection to bf16 in between (3 * 2^-8 of a head's length, and its
+    # bias; see test_heads_outside_the_epilogue)
+    oq = _oq()
+    d, Hq, Hk, rot = 384, 3, 1, D // 2
+    N = (Hq + Hk + 2) * D
+    plan = oq.Plan(d, 128, 2, seed=2, center=True)
+    x = to_torch_bf16(synth.make_x(T, d, mean_var=3.0, heavy_frac=0.0, seed=T))
+    prep = oq.prepare_weights_w8(plan, to_torch_bf16(synth.make_w(N, d)))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    qw, kw, qb, kb = (torch.randn(D, generator=g, device="cuda") for _ in range(4))
+    cos, sin = _tables(64, rot)
+    h = oq.Heads(D, Hq, Hk, norm=norm, q_weight=qw, q_bias=qb, k_weight=kw, k_bias=kb, rope=rope,
+                 cos=cos, sin=sin)
+    pos = torch.randint(-2, 70, (T,), generator=g, device="cuda", dtype=torch.int32)
+    pos[-1], pos[0] = 64, 63                         # the first past the table, the last in it
+    y = oq.linear_qkv(plan, h, x, *prep, positions=pos).unflatten(-1, (-1, D))
+    z = oq.linear_w8a8(plan, x, *prep).unflatten(-1, (-1, D))
+    assert torch.equal(y[:, Hq + Hk:], z[:, Hq + Hk:])
+    q, k = oq.qk_norm_rope(h, z[:, :Hq], z[:, Hq:Hq + Hk], positions=pos)
+    want, got = torch.cat([q, k], 1).double(), y[:, :Hq + Hk].double()
+    lost = pos >= 64
+    assert bool(torch.isnan(got[lost][..., :rot]).all())
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    got, want = got.nan_to_num(), want.nan_to_num()
+    # without the norm an element is as long as the layer's; the bias is not touched by the rounding
+    length = want.norm(dim=-1) + torch.cat([qb.norm().expand(Hq), kb.norm().expand(Hk)])
+    length = length + (z[:, :Hq + Hk].double() * torch.stack([qw] * Hq + [kw] * Hk)).norm(dim=-1) * (norm == "none")
+    assert bool(((got - want).norm(dim=-1) <= 3 * 2.0 ** -8 * length).all())
+    _ok(oq)
+    plan.close()
+
+
 def test_many_tokens_of_one_small_head():
     oq = _oq()
     cos, sin = _tables(16, 16)

@@ -127,7 +127,7 @@ constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
 
-// Heads formed in the epilogue (columns o < w.n_head): the parameters of HeadArgs
+// Heads formed in an epilogue (columns o < w.n_head): the parameters of HeadArgs
 struct TileHeads {
   int D, nq, norm, rope, rot;              // nq: query columns
   float eps, inv_d;
@@ -699,6 +699,20 @@ cudaError_t launch_beside(void (*kern)(P...), unsigned grid, unsigned threads, s
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+TileHeads head_params(const HeadArgs& a) {
+  TileHeads h{};
+  h.D = a.head_dim; h.nq = a.q.heads * a.head_dim;
+  h.norm = a.norm; h.rope = a.rope;
+  h.rot = a.rope == OQ_ROPE_NONE ? 0 : a.rot_dim;
+  h.eps = a.eps; h.inv_d = 1.f / (float)a.head_dim;
+  h.qw = a.q.weight; h.qb = a.q.bias;
+  h.kw = a.k.weight; h.kb = a.k.bias;
+  h.cos = a.cos; h.sin = a.sin; h.n_pos = a.n_pos;
+  h.positions = a.positions; h.pos_bs = a.pos_batch_stride;
+  h.seq = (int)a.seq;
+  return h;
+}
+
 oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   CUtensorMap ta, tb;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
@@ -717,15 +731,7 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   p.cw = CH;
   if (heads) {
     p.cw = heads->head_dim;
-    p.h.D = heads->head_dim; p.h.nq = heads->q.heads * heads->head_dim;
-    p.h.norm = heads->norm; p.h.rope = heads->rope;
-    p.h.rot = heads->rope == OQ_ROPE_NONE ? 0 : heads->rot_dim;
-    p.h.eps = heads->eps; p.h.inv_d = 1.f / (float)heads->head_dim;
-    p.h.qw = heads->q.weight; p.h.qb = heads->q.bias;
-    p.h.kw = heads->k.weight; p.h.kb = heads->k.bias;
-    p.h.cos = heads->cos; p.h.sin = heads->sin; p.h.n_pos = heads->n_pos;
-    p.h.positions = heads->positions; p.h.pos_bs = heads->pos_batch_stride;
-    p.h.seq = (int)heads->seq;
+    p.h = head_params(*heads);
   }
   p.maxch = TN / p.cw;
   p.npm = (w.N + p.cw - 1) / p.cw;
@@ -757,6 +763,7 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 // operands have the same one, so each 8 bytes a lane holds serve as its share of one MMA: four
 // MMAs per 128 bytes, no shuffles, whole 128-byte lines from every row.
 constexpr int kRowTokens = 32;             // tokens at most: four groups of the MMA's columns
+constexpr int kHeadRowTokens = 16;         // tokens at most with heads
 constexpr int RT = 256;                    // threads
 constexpr int RW = RT / 32;
 
@@ -796,6 +803,7 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 
 struct RowParams {
   W8Params w;
+  TileHeads h;             // heads formed by the blocks of a cluster
   bool wide_a, wide_w;     // the codes' bases are 32-byte aligned (their rows are: K % 32 == 0)
 };
 
@@ -810,21 +818,126 @@ __device__ __forceinline__ OutConst out_const(const W8Params& p, int t, int o) {
   c.b = p.bias ? __bfloat162float(p.bias[o]) : 0.f;
   return c;
 }
-__device__ __forceinline__ void out_store(const W8Params& p, int t, int o, int sum,
-                                          const OutConst& c) {
-  if (p.out_acc) {
-    reinterpret_cast<int32_t*>(p.out)[(int64_t)t * p.N + o] = sum;
-    return;
-  }
-  const float y = __fmaf_rn((float)sum, __fmul_rn(c.alpha, c.s), __fmaf_rn(c.mean, c.w1, c.b));
-  if (o < p.n_head)
-    p.head[(int64_t)t * p.n_head + o] = y;
-  else
-    reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)t * p.N + o] = __float2bfloat16_rn(y);
+__device__ __forceinline__ float out_value(int sum, const OutConst& c) {
+  return __fmaf_rn((float)sum, __fmul_rn(c.alpha, c.s), __fmaf_rn(c.mean, c.w1, c.b));
+}
+__device__ __forceinline__ void store_bf16(const W8Params& p, int t, int o, float y) {
+  reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)t * p.N + o] = __float2bfloat16_rn(y);
+}
+// a float in the shared memory of CTA `rank` of the cluster, at this CTA's address `mine`
+__device__ __forceinline__ float cluster_float(const float* mine, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+               : "=f"(v)
+               : "r"(dev::map_to_cta(dev::smem_u32(mine), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+// sum over the 16 lanes that hold a token's 16 channels
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
 }
 
-// NT groups of eight tokens; RU 128-byte segments of a warp in flight; blocks for RB to an SM
-template <int NT, int RU, int RB>
+// Heads of D <= 128 elements for few tokens: the D / 16 blocks that hold a head's channels are a
+// cluster. Each block's values and partial sums (of values, of squares) lie in its shared memory,
+// and every block reads the others'. Thread: channel oc of tokens tid / 16 + 16 e, y[e] its values.
+template <int NO, int MT>
+__device__ __forceinline__ void cluster_heads(const RowParams& rp, int o0, const float (&y)[NO],
+                                              const int64_t (&pos)[NO], const float (&cs)[NO],
+                                              const float (&sn)[NO], float (*s_y)[17],
+                                              float (*s_stat)[MT]) {
+  const W8Params& p = rp.w;
+  const TileHeads& h = rp.h;
+  const int tid = threadIdx.x, oc = tid & 15, C = h.D / 16, half = h.rot / 2;
+  const int rank = (int)dev::cluster_ctarank(), el = rank * 16 + oc;
+  const bool is_q = o0 < h.nq, layer = h.norm == OQ_NORM_LAYER;
+  const float* wt = is_q ? h.qw : h.kw;
+  const float* bs = is_q ? h.qb : h.kb;
+  const bool in_rot = el < h.rot;
+  const int other = h.rope == OQ_ROPE_PAIRS ? el ^ 1 : el < half ? el + half : el - half;
+  const float wv = wt ? wt[el] : 1.f, bv = bs ? bs[el] : 0.f;
+  const float wo = wt && in_rot ? wt[other] : 1.f, bo = bs && in_rot ? bs[other] : 0.f;
+  float m[NO], q[NO];
+#pragma unroll
+  for (int e = 0; e < NO; ++e) {
+    const int t = (tid >> 4) + 16 * e;
+    const float part = half_warp_sum(layer ? y[e] : y[e] * y[e]);
+    if (t < MT) {
+      s_y[t][oc] = y[e];
+      if (oc == 0) s_stat[0][t] = part;
+    }
+    m[e] = 0.f;
+  }
+  dev::cluster_sync();
+#pragma unroll
+  for (int e = 0; e < NO; ++e) {
+    const int t = min((tid >> 4) + 16 * e, MT - 1);
+    q[e] = 0.f;
+    for (int r = 0; r < C; ++r) q[e] += cluster_float(&s_stat[0][t], r);
+  }
+  if (layer) {
+#pragma unroll
+    for (int e = 0; e < NO; ++e) {
+      const int t = (tid >> 4) + 16 * e;
+      m[e] = q[e] * h.inv_d;
+      const float part = half_warp_sum((y[e] - m[e]) * (y[e] - m[e]));
+      if (oc == 0 && t < MT) s_stat[1][t] = part;
+    }
+    dev::cluster_sync();
+#pragma unroll
+    for (int e = 0; e < NO; ++e) {
+      const int t = min((tid >> 4) + 16 * e, MT - 1);
+      q[e] = 0.f;
+      for (int r = 0; r < C; ++r) q[e] += cluster_float(&s_stat[1][t], r);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < NO; ++e) {
+    const int t = (tid >> 4) + 16 * e;
+    if (t >= p.T) break;
+    const float r = h.norm == OQ_NORM_NONE ? 1.f : rsqrtf(fmaf(q[e], h.inv_d, h.eps));
+    const float n = fmaf((y[e] - m[e]) * r, wv, bv);
+    float out = n;
+    if (in_rot && pos[e] >= 0) {
+      const float no = fmaf((cluster_float(&s_y[t][other & 15], other >> 4) - m[e]) * r, wo, bo);
+      const bool low = h.rope == OQ_ROPE_PAIRS ? !(el & 1) : el < half;
+      out = low ? n * cs[e] - no * sn[e] : n * cs[e] + no * sn[e];
+    }
+    store_bf16(p, t, o0 + oc, out);
+  }
+  __syncwarp();
+  dev::cluster_sync();   // no block leaves while another still reads its values
+}
+
+// Position and angle of this thread's elements; they do not come from the launch before.
+template <int NO>
+__device__ __forceinline__ void row_angles(const RowParams& rp, int64_t (&pos)[NO], float (&cs)[NO],
+                                           float (&sn)[NO]) {
+  const TileHeads& h = rp.h;
+  const int half = h.rot / 2;
+  const int el = (int)dev::cluster_ctarank() * 16 + ((int)threadIdx.x & 15);
+  const int i = h.rope == OQ_ROPE_PAIRS ? el / 2 : el < half ? el : el - half;
+#pragma unroll
+  for (int e = 0; e < NO; ++e) {
+    const int t = ((int)threadIdx.x >> 4) + 16 * e;
+    pos[e] = -1;
+    cs[e] = sn[e] = __int_as_float(0x7fc00000);   // a position past the table
+    if (t < rp.w.T && el < h.rot) {
+      const int b = t / h.seq, s = t - b * h.seq;
+      pos[e] = h.positions ? (int64_t)h.positions[b * h.pos_bs + s] : s;
+      if (pos[e] >= 0 && pos[e] < h.n_pos) {
+        cs[e] = h.cos[pos[e] * half + i];
+        sn[e] = h.sin[pos[e] * half + i];
+      }
+    }
+  }
+}
+
+// NT groups of eight tokens; RU 128-byte segments of a warp in flight; blocks for RB to an SM.
+// HEADS: a cluster's blocks form a head (cluster_heads).
+template <int NT, int RU, int RB, bool HEADS>
 __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__ RowParams rp) {
   const W8Params& p = rp.w;
   __shared__ int s_part[RW][NT * 8][17];   // [warp][token][channel], one word of padding
@@ -841,6 +954,10 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
   const int oc = tid & 15;
   OutConst c0 = {};
   dependents_begin();
+  if (HEADS && o0 >= p.N) return;   // the last cluster's spare blocks, behind all heads
+  const bool head = HEADS && o0 < p.n_head;   // the same for a cluster's blocks
+  int64_t pos[NO];
+  float cs[NO], sn[NO];
   bool waited = false;
   int acc[NT][4] = {};
   for (int s0 = warp; s0 < segs; s0 += RW * RU) {
@@ -853,6 +970,7 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
       wr[u][1] = load32(w1 + k, in, rp.wide_w);
     }
     if (!waited) {   // the first weights are on their way
+      if (head) row_angles<NO>(rp, pos, cs, sn);
       dependency_wait();
       waited = true;
       if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
@@ -875,6 +993,7 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
                  x[u][n].v[j], x[u][n].v[j + 1]);
   }
   if (!waited) {   // a warp without a segment
+    if (head) row_angles<NO>(rp, pos, cs, sn);
     dependency_wait();
     if (NO == 1 && (tid >> 4) < p.T) c0 = out_const(p, tid >> 4, o0 + oc);
   }
@@ -887,40 +1006,64 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
     s_part[warp][n * 8 + 2 * i + 1][g + 8] = acc[n][3];
   }
   __syncthreads();
+  float y[NO] = {};
 #pragma unroll
   for (int e = 0; e < NO; ++e) {
-    const int t = (tid >> 4) + 16 * e;
+    const int t = (tid >> 4) + 16 * e, o = o0 + oc;
     if (t >= p.T) break;   // T <= 8 NT
     int sum = 0;
 #pragma unroll
     for (int q = 0; q < RW; ++q) sum += s_part[q][t][oc];
-    out_store(p, t, o0 + oc, sum, NO == 1 ? c0 : out_const(p, t, o0 + oc));
+    if (!HEADS && p.out_acc) {
+      reinterpret_cast<int32_t*>(p.out)[(int64_t)t * p.N + o] = sum;
+      continue;
+    }
+    y[e] = out_value(sum, NO == 1 ? c0 : out_const(p, t, o));
+    if (!HEADS && o < p.n_head)
+      p.head[(int64_t)t * p.n_head + o] = y[e];
+    else if (!head)
+      store_bf16(p, t, o, y[e]);
+  }
+  if constexpr (HEADS) {
+    __shared__ float s_y[NT * 8][17], s_stat[2][NT * 8];
+    __syncwarp();
+    if (head) cluster_heads<NO, NT * 8>(rp, o0, y, pos, cs, sn, s_y, s_stat);
   }
 }
 
-template <int NT>
+template <int NT, bool HEADS>
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
   // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
   // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
   // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
   // (8 tokens) 4.6 against 6.0. 16 tokens: 4096 x 4096 6.6 against 6.9; the other way
   // 4096 x 12288 13.7 against 14.6, 1920 x 5760 (24 tokens) 6.4 against 8.0.
-  const unsigned grid = (unsigned)(p.w.N / 16);
+  const unsigned cluster = HEADS ? (unsigned)p.h.D / 16u : 1u;
+  const unsigned grid = ((unsigned)(p.w.N / 16) + cluster - 1) / cluster * cluster;
   constexpr int D = NT == 1 ? 2 : 1;
-  if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)device_sms())
-    return launch_beside(k_gemm_w8_rows<NT, 2 * D, 2>, grid, RT, 0, 1, p.w.dependent, s, p);
-  return launch_beside(k_gemm_w8_rows<NT, D, 3>, grid, RT, 0, 1, p.w.dependent, s, p);
+  // Clusters (heads) want the room: 4096 -> 6144, one token, 9.9 us with the rotation in front against 13.2.
+  if constexpr (!HEADS)
+    if (p.w.K >= 4096 && grid <= 2u * 2u * (unsigned)device_sms())
+      return launch_beside(k_gemm_w8_rows<NT, 2 * D, 2, false>, grid, RT, 0, cluster, p.w.dependent,
+                           s, p);
+  return launch_beside(k_gemm_w8_rows<NT, D, 3, HEADS>, grid, RT, 0, cluster, p.w.dependent, s, p);
 }
 
-oq_status run_rows(const W8Params& w, cudaStream_t s) {
-  RowParams p;
+oq_status run_rows(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
+  RowParams p{};
   p.w = w;
   p.wide_a = (reinterpret_cast<uintptr_t>(w.a) & 31u) == 0;
   p.wide_w = (reinterpret_cast<uintptr_t>(w.w) & 31u) == 0;
-  const cudaError_t e = w.T <= 8    ? launch_rows<1>(p, s)
-                        : w.T <= 16 ? launch_rows<2>(p, s)
-                        : w.T <= 24 ? launch_rows<3>(p, s)
-                                    : launch_rows<4>(p, s);
+  cudaError_t e;
+  if (heads) {
+    p.h = head_params(*heads);
+    e = w.T <= 8 ? launch_rows<1, true>(p, s) : launch_rows<2, true>(p, s);
+  } else {
+    e = w.T <= 8    ? launch_rows<1, false>(p, s)
+        : w.T <= 16 ? launch_rows<2, false>(p, s)
+        : w.T <= 24 ? launch_rows<3, false>(p, s)
+                    : launch_rows<4, false>(p, s);
+  }
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_rows");
 }
 
@@ -1218,6 +1361,9 @@ double tiles_us(const W8Params& w) {
 }  // namespace
 
 bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim) {
+  // Rows: a cluster of at most eight blocks. Past 16 tokens the separate head kernel is as fast (32
+  // tokens, 4096 -> 6144: 15.9 us both; 16 tokens: 11.9 against 13.8).
+  if (T <= kHeadRowTokens) return head_dim <= 128;
   return T > kSplitTokens && head_dim % 32 == 0 && (rope == OQ_ROPE_NONE || rot_dim % 32 == 0);
 }
 
@@ -1232,10 +1378,11 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");
   p.limit_ns = kWaitLimitNs;
-  // heads come with tiles only (gemm_w8_forms_heads)
-  if (g.T > kSplitTokens || g.heads) return run_tiles(p, g.heads, s);
+  // heads come with rows and with tiles (gemm_w8_forms_heads)
+  if (g.heads && g.T <= kHeadRowTokens) return run_rows(p, g.heads, s);
+  if (g.heads || g.T > kSplitTokens) return run_tiles(p, g.heads, s);
   const SplitPlan split = plan_split(p);
-  if (g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, s);
+  if (g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, nullptr, s);
   if (split.S > 0 && split.us <= tiles_us(p)) return run_split(p, split, s);
   return run_tiles(p, nullptr, s);
 }
