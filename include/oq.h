@@ -448,7 +448,8 @@ oq_status oq_qk_norm_rope(const oq_heads* heads, int64_t batch, int64_t seq, con
                           const int64_t q_out_strides[3], void* k_out,
                           const int64_t k_out_strides[3], void* stream);
 
-/* Bytes of device workspace oq_linear_qkv needs (0 for invalid arguments). */
+/* Bytes of device workspace that are enough for oq_linear_qkv with T tokens (INT8 weights: or with
+ * fewer); 0 for invalid arguments. */
 size_t oq_linear_qkv_workspace_bytes(const oq_plan* plan, const oq_heads* heads,
                                      oq_weight_kind weights, int64_t T, int64_t d_out);
 

@@ -183,6 +183,29 @@ def test_projection_around_its_shapes(T, D, rope, norm):
     plan.close()
 
 
+@pytest.mark.parametrize("D,rot", [(64, 64), (80, 80), (256, 256)])
+def test_one_workspace_for_every_number_of_tokens(D, rot):
+    # sized for the most tokens, used for fewer
+    oq = _oq()
+    d, Hq, Hk = 256, 3, 2
+    N = (Hq + 2 * Hk) * D
+    plan = oq.Plan(d, 256, 2, center=True)
+    prep = oq.prepare_weights_w8(plan, to_torch_bf16(synth.make_w(N, d)))
+    cos, sin = _tables(512, rot)
+    h = oq.Heads(D, Hq, Hk, rope="pairs", cos=cos, sin=sin)
+    need = [oq.lib().oq_linear_qkv_workspace_bytes(plan.handle, h._ref, 1, T, N) for T in range(0, 520)]
+    assert all(a <= b for a, b in zip(need, need[1:]))
+    for most in (512, 256, 20):
+        ws = torch.empty(need[most], dtype=torch.uint8, device="cuda")
+        for T in (most, 300, 256, 100, 17, 16, 1):
+            if T <= most:
+                x = to_torch_bf16(synth.make_x(T, d, mean_var=3.0, heavy_frac=0.0, seed=T))
+                y = oq.linear_qkv(plan, h, x, *prep, workspace=ws)
+                assert torch.equal(y, oq.linear_qkv(plan, h, x, *prep))
+    _ok(oq)
+    plan.close()
+
+
 def test_many_tokens_of_one_small_head():
     oq = _oq()
     cos, sin = _tables(16, 16)

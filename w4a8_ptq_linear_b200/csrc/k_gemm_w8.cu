@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "oq_internal.h"
@@ -1078,7 +1079,7 @@ oq_status run_rows(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 constexpr int PT = 256;                    // threads
 constexpr int PM = 128;                    // channels of a cluster
 constexpr int PWB = PM * 128;              // weight bytes of a K block
-constexpr int kSplitTokens = 256;          // tokens at most
+constexpr int kSplitTokens = kGemmW8FewTokens;   // tokens at most
 constexpr int kSplitMax = 8;               // CTAs of a cluster at most (portable size)
 constexpr int kRingMax = 12;               // stages at most
 
@@ -1367,7 +1368,7 @@ bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim) {
   return T > kSplitTokens && head_dim % 32 == 0 && (rope == OQ_ROPE_NONE || rot_dim % 32 == 0);
 }
 
-oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
+oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) try {
   if (g.T == 0) return OQ_OK;
   W8Params p{};
   p.a = g.a; p.w = g.w; p.a_scale = g.a_scale; p.mean = g.mean; p.w_scale = g.w_scale;
@@ -1385,6 +1386,8 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) {
   if (g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, nullptr, s);
   if (split.S > 0 && split.us <= tiles_us(p)) return run_split(p, split, s);
   return run_tiles(p, nullptr, s);
+} catch (const std::bad_alloc&) {   // of the kept launch shapes
+  return fail(OQ_ERR_NOMEM, "host allocation");
 }
 
 }  // namespace oq

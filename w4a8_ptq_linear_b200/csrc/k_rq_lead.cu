@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "oq_internal.h"
@@ -44,7 +45,7 @@ const void* lead_kernel(int hlog2) {
 
 }  // namespace
 
-oq_status launch_rotate_quant_lead(const RqArgs& a, cudaStream_t s) {
+oq_status launch_rotate_quant_lead(const RqArgs& a, cudaStream_t s) try {
   if (a.mode != kRqInt8 || a.d > kRqPairMaxD)
     return fail(OQ_ERR_UNSUPPORTED, "leading rotate-quantize: INT8 absmax, d <= %d", kRqPairMaxD);
   if (a.T == 0) return OQ_OK;
@@ -80,6 +81,8 @@ oq_status launch_rotate_quant_lead(const RqArgs& a, cudaStream_t s) {
   void* args[] = {&p};
   const cudaError_t e = cudaLaunchKernel(fn, dim3(grid), dim3((unsigned)threads), args, smem, s);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch rq_lead");
+} catch (const std::bad_alloc&) {   // of the kept launch shapes
+  return fail(OQ_ERR_NOMEM, "host allocation");
 }
 
 }  // namespace oq

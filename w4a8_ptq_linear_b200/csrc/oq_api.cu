@@ -1,5 +1,6 @@
 // C ABI of the rotated, quantized linear layer (declarations and contracts: include/oq.h).
 // Host-side validation, plan lifecycle, the device error word and dispatch to the kernels.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -940,7 +941,10 @@ size_t oq_linear_qkv_workspace_bytes(const oq_plan* plan, const oq_heads* heads,
                                      oq_weight_kind weights, int64_t T, int64_t d_out) {
   (void)d_out;
   if (!plan || T < 0 || T > 0x7FFFFFFF || check_heads(heads) != OQ_OK) return 0;
-  return oq_linear_workspace_bytes(plan, T) + head_bytes(heads, weights, T);
+  // enough for fewer tokens too, whose heads may not be formed in the GEMM
+  const int64_t few = std::min<int64_t>(T, kGemmW8FewTokens);
+  return oq_linear_workspace_bytes(plan, T) +
+         std::max(head_bytes(heads, weights, T), head_bytes(heads, weights, few));
 }
 
 oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* x_bf16,
@@ -966,7 +970,7 @@ oq_status oq_linear_qkv(const oq_plan* plan, const oq_heads* heads, const void* 
     return fail(OQ_ERR_INVALID_ARG, "d_out=%lld holds fewer than the %lld query and key columns",
                 (long long)d_out, (long long)n_head);
   st = check_layer(plan, T, w_rowsum, workspace, workspace_bytes,
-                   oq_linear_qkv_workspace_bytes(plan, heads, weights, T, d_out));
+                   oq_linear_workspace_bytes(plan, T) + head_bytes(heads, weights, T));
   if (st != OQ_OK) return st;
   st = check_positions(positions, pos_batch_stride);
   if (st != OQ_OK) return st;

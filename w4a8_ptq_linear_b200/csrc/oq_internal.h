@@ -206,6 +206,8 @@ struct GemmW8Args {
   bool dependent = false;
 };
 oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s);
+// Tokens up to which the GEMM may run in a shape for few of them.
+constexpr int kGemmW8FewTokens = 256;
 // Whether the GEMM for T tokens can form these heads in its epilogue.
 bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim);
 
