@@ -1076,6 +1076,8 @@ oq_status run_rows(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 // tokens by another; the int32 partial sums go from TMEM to shared memory, and after a cluster
 // barrier CTA r adds its share of the tokens from all S CTAs through distributed shared memory.
 // Whole numbers add exactly in any order, so the result is that of the other shapes bit for bit.
+// 40 x 4096 x 4096 9.5 us, 128 x 4096 x 12288 18.7, 256 x 12288 x 4096 21.8; a CTA's start, the barriers
+// and the end are 6 to 10 us of that, a K block 0.36 us.
 constexpr int PT = 256;                    // threads
 constexpr int PM = 128;                    // channels of a cluster
 constexpr int PWB = PM * 128;              // weight bytes of a K block
@@ -1085,12 +1087,119 @@ constexpr int kRingMax = 12;               // stages at most
 
 struct SplitParams {
   W8Params w;
+  TileHeads h;                             // heads formed in the epilogue (HEADS)
   int npad;                                // tokens, rounded up to 16 (the MMA's N)
   int tcols;                               // TMEM columns: a power of two >= 32
   int ks, nkb, ns;                         // K blocks of a CTA, in all; stages
   int off_bar;                             // ring and partial sums lie in front of the barriers
 };
 
+// Heads of D elements, D a divisor of 128, in the epilogue of the split: a lane holds four channels (o
+// ... o + 3) of one token, D / 4 neighbouring lanes a head. The token is the warp's.
+struct LaneHead {
+  float4 wv, bv;
+  int el;         // first element of this lane in its head
+  bool head;
+};
+__device__ __forceinline__ LaneHead lane_head(const SplitParams& sp, int o) {
+  const TileHeads& h = sp.h;
+  LaneHead l;
+  l.head = o < sp.w.n_head;
+  l.el = o % h.D;
+  const float* wt = o < h.nq ? h.qw : h.kw;
+  const float* bs = o < h.nq ? h.qb : h.kb;
+  l.wv = l.head && wt ? *reinterpret_cast<const float4*>(wt + l.el) : make_float4(1.f, 1.f, 1.f, 1.f);
+  l.bv = l.head && bs ? *reinterpret_cast<const float4*>(bs + l.el) : make_float4(0.f, 0.f, 0.f, 0.f);
+  return l;
+}
+// the angle of a token at position pos for the lane's channels: cosines, and sines with their signs
+struct LaneAngle {
+  float4 c, s;
+  bool turn;
+};
+__device__ __forceinline__ LaneAngle lane_angle(const SplitParams& sp, const LaneHead& l, int pos) {
+  const TileHeads& h = sp.h;
+  const int half = h.rot / 2;
+  const bool low = l.el < half;
+  LaneAngle a;
+  a.turn = l.head && l.el < h.rot && pos >= 0;
+  const float nan = __int_as_float(0x7fc00000);   // a position past the table
+  a.c = a.s = make_float4(nan, nan, nan, nan);
+  if (a.turn && pos < h.n_pos) {
+    if (h.rope == OQ_ROPE_PAIRS) {
+      const float2 c2 = *reinterpret_cast<const float2*>(h.cos + (int64_t)pos * half + l.el / 2);
+      const float2 s2 = *reinterpret_cast<const float2*>(h.sin + (int64_t)pos * half + l.el / 2);
+      a.c = make_float4(c2.x, c2.x, c2.y, c2.y);
+      a.s = make_float4(-s2.x, s2.x, -s2.y, s2.y);
+    } else {
+      const int i = low ? l.el : l.el - half;
+      a.c = *reinterpret_cast<const float4*>(h.cos + (int64_t)pos * half + i);
+      a.s = *reinterpret_cast<const float4*>(h.sin + (int64_t)pos * half + i);
+      if (low) a.s = make_float4(-a.s.x, -a.s.y, -a.s.z, -a.s.w);
+    }
+  }
+  return a;
+}
+// The values of the lane's channels of TU tokens, step by step for all of them (the steps of one wait
+// for each other's shuffles); y stays where the lane holds no head.
+template <int TU>
+__device__ __forceinline__ void lane_heads(const SplitParams& sp, const LaneHead& l,
+                                           const LaneAngle (&a)[TU], int lane, float4 (&y)[TU]) {
+  const TileHeads& h = sp.h;
+  const int lanes = h.D / 4, half = h.rot / 2;
+  auto group_sums = [&](float (&v)[TU]) {
+    for (int m = lanes / 2; m > 0; m >>= 1) {
+#pragma unroll
+      for (int u = 0; u < TU; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], m);
+    }
+  };
+  float4 n[TU];
+  float q[TU], r[TU];
+#pragma unroll
+  for (int u = 0; u < TU; ++u) {
+    n[u] = y[u];
+    q[u] = (y[u].x + y[u].y) + (y[u].z + y[u].w);
+  }
+  if (h.norm == OQ_NORM_LAYER) {
+    group_sums(q);
+#pragma unroll
+    for (int u = 0; u < TU; ++u) {
+      const float m = q[u] * h.inv_d;
+      n[u] = make_float4(y[u].x - m, y[u].y - m, y[u].z - m, y[u].w - m);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < TU; ++u) {
+    q[u] = fmaf(n[u].x, n[u].x, n[u].y * n[u].y) + fmaf(n[u].z, n[u].z, n[u].w * n[u].w);
+    r[u] = 1.f;
+  }
+  if (h.norm != OQ_NORM_NONE) {
+    group_sums(q);
+#pragma unroll
+    for (int u = 0; u < TU; ++u) r[u] = rsqrtf(fmaf(q[u], h.inv_d, h.eps));
+  }
+  // the other half's lanes
+  const int mate = l.el >= h.rot ? lane : l.el < half ? lane + half / 4 : lane - half / 4;
+#pragma unroll
+  for (int u = 0; u < TU; ++u) {
+    n[u] = make_float4(fmaf(n[u].x * r[u], l.wv.x, l.bv.x), fmaf(n[u].y * r[u], l.wv.y, l.bv.y),
+                       fmaf(n[u].z * r[u], l.wv.z, l.bv.z), fmaf(n[u].w * r[u], l.wv.w, l.bv.w));
+    float4 o = make_float4(n[u].y, n[u].x, n[u].w, n[u].z);
+    if (h.rope != OQ_ROPE_PAIRS) {
+      o.x = __shfl_sync(0xffffffffu, n[u].x, mate);
+      o.y = __shfl_sync(0xffffffffu, n[u].y, mate);
+      o.z = __shfl_sync(0xffffffffu, n[u].z, mate);
+      o.w = __shfl_sync(0xffffffffu, n[u].w, mate);
+    }
+    if (!l.head) continue;
+    y[u] = n[u];
+    if (a[u].turn)
+      y[u] = make_float4(fmaf(n[u].x, a[u].c.x, o.x * a[u].s.x), fmaf(n[u].y, a[u].c.y, o.y * a[u].s.y),
+                         fmaf(n[u].z, a[u].c.z, o.z * a[u].s.z), fmaf(n[u].w, a[u].c.w, o.w * a[u].s.w));
+  }
+}
+
+template <bool HEADS>
 __global__ void __launch_bounds__(PT)
     k_gemm_w8_split(const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_a,
@@ -1103,6 +1212,7 @@ __global__ void __launch_bounds__(PT)
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kRingMax + 1);   // TMEM base, abort
   volatile uint32_t* s_abort = misc + 1;
   float2* s_tok = reinterpret_cast<float2*>(smem + sp.off_bar + 256);
+  int* s_pos = reinterpret_cast<int*>(s_tok + kSplitTokens);   // HEADS: the tokens' positions
   dependents_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int S = (int)dev::cluster_nctarank(), r = (int)dev::cluster_ctarank();
@@ -1174,6 +1284,11 @@ __global__ void __launch_bounds__(PT)
   const int per = (p.T + S - 1) / S, t0 = min(p.T, r * per), t1 = min(p.T, t0 + per);
   for (int t = t0 + tid; t < t1; t += PT)
     s_tok[t - t0] = make_float2(p.a_scale[t], p.mean ? p.mean[t] : 0.f);
+  if constexpr (HEADS)
+    for (int t = t0 + tid; t < t1; t += PT) {
+      const int b = t / sp.h.seq, st = t - b * sp.h.seq;
+      s_pos[t - t0] = sp.h.positions ? sp.h.positions[b * sp.h.pos_bs + st] : st;
+    }
   const int o = o0 + lane * 4;
   const bool has = o < p.N;   // N % 16 == 0: the four channels lie all inside or all outside
   float2 cs[2], cw[2], cb[2];
@@ -1186,6 +1301,9 @@ __global__ void __launch_bounds__(PT)
                                         __bfloat162float(p.bias[o + 2 * i + 1]))
                           : make_float2(0.f, 0.f);
   }
+
+  LaneHead lh = {};
+  if constexpr (HEADS) lh = lane_head(sp, o);
 
   // ---- partial sums: TMEM -> shared memory, int32 [token][128 channels] ----
   {
@@ -1210,11 +1328,17 @@ __global__ void __launch_bounds__(PT)
   // ---- sum over the cluster and epilogue: a warp takes a token's 128 channels ----
   {
     const uint32_t mine = dev::smem_u32(smem) + (uint32_t)lane * 16u;
-    constexpr int TU = 2;   // tokens of a warp whose remote loads are in flight together
+    constexpr int TU = 2;   // tokens of a warp whose loads are in flight together
     for (int tb = t0 + warp; tb < t1; tb += TU * (PT / 32)) {
       int4 sum[TU];
 #pragma unroll
       for (int u = 0; u < TU; ++u) sum[u] = make_int4(0, 0, 0, 0);
+      LaneAngle angle[TU];
+      if constexpr (HEADS) {
+#pragma unroll
+        for (int u = 0; u < TU; ++u)
+          angle[u] = lane_angle(sp, lh, s_pos[min(tb + u * (PT / 32), t1 - 1) - t0]);
+      }
 #pragma unroll
       for (int sr = 0; sr < kSplitMax; ++sr) {
         if (sr >= S) break;
@@ -1229,26 +1353,30 @@ __global__ void __launch_bounds__(PT)
           }
         }
       }
+      float4 y[TU];
 #pragma unroll
       for (int u = 0; u < TU; ++u) {
         const int t = tb + u * (PT / 32);
-        if (t >= t1 || !has) continue;
-        if (p.out_acc) {
-          *reinterpret_cast<int4*>(reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o) = sum[u];
-          continue;
-        }
-        const float2 tk = s_tok[t - t0];
+        const float2 tk = s_tok[min(t, t1 - 1) - t0];
         const float2 al = make_float2(tk.x, tk.x), mn = make_float2(tk.y, tk.y);
         const float2 y0 = __ffma2_rn(make_float2((float)sum[u].x, (float)sum[u].y),
                                      __fmul2_rn(al, cs[0]), __ffma2_rn(mn, cw[0], cb[0]));
         const float2 y1 = __ffma2_rn(make_float2((float)sum[u].z, (float)sum[u].w),
                                      __fmul2_rn(al, cs[1]), __ffma2_rn(mn, cw[1], cb[1]));
-        if (o < p.n_head)
-          *reinterpret_cast<float4*>(p.head + (int64_t)t * p.n_head + o) =
-              make_float4(y0.x, y0.y, y1.x, y1.y);
+        y[u] = make_float4(y0.x, y0.y, y1.x, y1.y);
+      }
+      if constexpr (HEADS) lane_heads<TU>(sp, lh, angle, lane, y);
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
+        const int t = tb + u * (PT / 32);
+        if (t >= t1 || !has) continue;
+        if (!HEADS && p.out_acc)
+          *reinterpret_cast<int4*>(reinterpret_cast<int32_t*>(p.out) + (int64_t)t * p.N + o) = sum[u];
+        else if (!HEADS && o < p.n_head)
+          *reinterpret_cast<float4*>(p.head + (int64_t)t * p.n_head + o) = y[u];
         else
           *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + (int64_t)t * p.N + o) =
-              make_uint2(pack2(y0), pack2(y1));
+              make_uint2(pack2(make_float2(y[u].x, y[u].y)), pack2(make_float2(y[u].z, y[u].w)));
       }
     }
   }
@@ -1274,7 +1402,7 @@ struct SplitPlan {
 
 SplitPlan plan_split(const W8Params& w) {
   const int npad = (w.T + 15) / 16 * 16, nkb = (w.K + 127) / 128, tiles = (w.N + PM - 1) / PM;
-  const void* kern = reinterpret_cast<const void*>(&k_gemm_w8_split);
+  const void* kern = reinterpret_cast<const void*>(&k_gemm_w8_split<false>);
   static std::mutex mu;
   static std::map<std::tuple<int, int, int, int>, SplitPlan> kept;
   SplitPlan best;
@@ -1298,7 +1426,7 @@ SplitPlan plan_split(const W8Params& w) {
     const int room = npad <= 192 ? 108 * 1024 : 216 * 1024;
     c.ns = std::min(std::min(c.ks, kRingMax), room / stage);
     c.off_bar = (std::max(c.ns * stage, npad * PM * 4) + 1023) / 1024 * 1024;
-    c.smem = c.off_bar + 256 + 8 * kSplitTokens + 1024;
+    c.smem = c.off_bar + 256 + 12 * kSplitTokens + 1024;
     if (resident_clusters(kern, S, c.smem, PT) <= 0) continue;   // does not launch here
     // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
     // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
@@ -1318,9 +1446,11 @@ SplitPlan plan_split(const W8Params& w) {
   return best;
 }
 
-oq_status run_split(const W8Params& w, const SplitPlan& plan, cudaStream_t s) {
+oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* heads,
+                    cudaStream_t s) {
   SplitParams p{};
   p.w = w;
+  if (heads) p.h = head_params(*heads);
   p.npad = (w.T + 15) / 16 * 16;
   p.tcols = 32;
   while (p.tcols < p.npad) p.tcols *= 2;
@@ -1336,8 +1466,11 @@ oq_status run_split(const W8Params& w, const SplitPlan& plan, cudaStream_t s) {
                   CU_TENSOR_MAP_SWIZZLE_128B))
     return fail(OQ_ERR_CUDA, "cuTensorMapEncodeTiled failed or unavailable");
   const int tiles = (w.N + PM - 1) / PM;
-  const cudaError_t e = launch_beside(k_gemm_w8_split, (unsigned)(tiles * plan.S), PT,
-                                      (size_t)plan.smem, (unsigned)plan.S, w.dependent, s, tw, ta, p);
+  const auto kern = heads ? &k_gemm_w8_split<true> : &k_gemm_w8_split<false>;
+  cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8_split)");
+  e = launch_beside(kern, (unsigned)(tiles * plan.S), PT, (size_t)plan.smem, (unsigned)plan.S,
+                    w.dependent, s, tw, ta, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_split");
 }
 
@@ -1361,11 +1494,20 @@ double tiles_us(const W8Params& w) {
 
 }  // namespace
 
+namespace {
+bool tiles_form(int head_dim, int rope, int rot_dim) {
+  return head_dim % 32 == 0 && (rope == OQ_ROPE_NONE || rot_dim % 32 == 0);
+}
+}  // namespace
+
+// Forming the heads saves a launch, about 3 us of the host's time. On the GPU, with the rotation in
+// front, against the head kernel behind: 4096 -> 6144 with 1 token 9.9 us against 11.2, 16 tokens 11.9
+// against 13.8, 32 tokens 13.2 against 15.6, 64 tokens 14.3 against 15.4; 1920 -> 5760 with 24 tokens
+// 11.5 against 11.3, 128 tokens 16.9 against 15.5.
 bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim) {
-  // Rows: a cluster of at most eight blocks. Past 16 tokens the separate head kernel is as fast (32
-  // tokens, 4096 -> 6144: 15.9 us both; 16 tokens: 11.9 against 13.8).
-  if (T <= kHeadRowTokens) return head_dim <= 128;
-  return T > kSplitTokens && head_dim % 32 == 0 && (rope == OQ_ROPE_NONE || rot_dim % 32 == 0);
+  if (T <= kHeadRowTokens) return head_dim <= 128;    // a cluster of at most eight blocks
+  if (T <= kSplitTokens) return PM % head_dim == 0;   // whole heads in a cluster's channels
+  return tiles_form(head_dim, rope, rot_dim);
 }
 
 oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) try {
@@ -1379,13 +1521,15 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) try {
   p.err = device_error_word();
   if (!p.err) return fail(OQ_ERR_CUDA, "device error word unavailable");
   p.limit_ns = kWaitLimitNs;
-  // heads come with rows and with tiles (gemm_w8_forms_heads)
+  if (g.T > kSplitTokens) return run_tiles(p, g.heads, s);
+  // with heads: rows up to 16 tokens (a cluster of up to eight blocks each), then the split
   if (g.heads && g.T <= kHeadRowTokens) return run_rows(p, g.heads, s);
-  if (g.heads || g.T > kSplitTokens) return run_tiles(p, g.heads, s);
   const SplitPlan split = plan_split(p);
-  if (g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, nullptr, s);
-  if (split.S > 0 && split.us <= tiles_us(p)) return run_split(p, split, s);
-  return run_tiles(p, nullptr, s);
+  if (!g.heads && g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, nullptr, s);
+  const bool tiles = !g.heads || tiles_form(g.heads->head_dim, g.heads->rope, g.heads->rot_dim);
+  if (split.S > 0 && (!tiles || split.us <= tiles_us(p))) return run_split(p, split, g.heads, s);
+  if (tiles) return run_tiles(p, g.heads, s);
+  return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no cluster fits on this device");
 } catch (const std::bad_alloc&) {   // of the kept launch shapes
   return fail(OQ_ERR_NOMEM, "host allocation");
 }
