@@ -1238,6 +1238,23 @@ __global__ void __launch_bounds__(PT)
     dev::tmem_alloc(dev::smem_u32(&misc[0]), (uint32_t)sp.tcols);
     dev::tmem_relinquish();
   }
+  // this CTA's share of the tokens; this lane's four channels. What does not come from the launch before
+  // is read before dependency_wait(), while that runs (0.2 us of 13).
+  const int per = (p.T + S - 1) / S, t0 = min(p.T, r * per), t1 = min(p.T, t0 + per);
+  const int o = o0 + lane * 4;
+  const bool has = o < p.N;   // N % 16 == 0: the four channels lie all inside or all outside
+  float2 cs[2], cw[2], cb[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    cs[i] = has ? make_float2(p.w_scale[o + 2 * i], p.w_scale[o + 2 * i + 1]) : make_float2(0.f, 0.f);
+    cw[i] = has && p.mean ? make_float2(p.w_rowsum[o + 2 * i], p.w_rowsum[o + 2 * i + 1])
+                          : make_float2(0.f, 0.f);
+    cb[i] = has && p.bias ? make_float2(__bfloat162float(p.bias[o + 2 * i]),
+                                        __bfloat162float(p.bias[o + 2 * i + 1]))
+                          : make_float2(0.f, 0.f);
+  }
+  LaneHead lh = {};
+  if constexpr (HEADS) lh = lane_head(sp, o);
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
@@ -1278,32 +1295,14 @@ __global__ void __launch_bounds__(PT)
     }
     dev::mma_commit(done);   // arrives once every MMA issued above has completed
   }
-  if (warp != 2) dependency_wait();
-
-  // this CTA's share of the tokens, their scales and means; this lane's four channels
-  const int per = (p.T + S - 1) / S, t0 = min(p.T, r * per), t1 = min(p.T, t0 + per);
-  for (int t = t0 + tid; t < t1; t += PT)
-    s_tok[t - t0] = make_float2(p.a_scale[t], p.mean ? p.mean[t] : 0.f);
   if constexpr (HEADS)
     for (int t = t0 + tid; t < t1; t += PT) {
       const int b = t / sp.h.seq, st = t - b * sp.h.seq;
       s_pos[t - t0] = sp.h.positions ? sp.h.positions[b * sp.h.pos_bs + st] : st;
     }
-  const int o = o0 + lane * 4;
-  const bool has = o < p.N;   // N % 16 == 0: the four channels lie all inside or all outside
-  float2 cs[2], cw[2], cb[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    cs[i] = has ? make_float2(p.w_scale[o + 2 * i], p.w_scale[o + 2 * i + 1]) : make_float2(0.f, 0.f);
-    cw[i] = has && p.mean ? make_float2(p.w_rowsum[o + 2 * i], p.w_rowsum[o + 2 * i + 1])
-                          : make_float2(0.f, 0.f);
-    cb[i] = has && p.bias ? make_float2(__bfloat162float(p.bias[o + 2 * i]),
-                                        __bfloat162float(p.bias[o + 2 * i + 1]))
-                          : make_float2(0.f, 0.f);
-  }
-
-  LaneHead lh = {};
-  if constexpr (HEADS) lh = lane_head(sp, o);
+  if (warp != 2) dependency_wait();
+  for (int t = t0 + tid; t < t1; t += PT)
+    s_tok[t - t0] = make_float2(p.a_scale[t], p.mean ? p.mean[t] : 0.f);
 
   // ---- partial sums: TMEM -> shared memory, int32 [token][128 channels] ----
   {
@@ -1502,8 +1501,8 @@ bool tiles_form(int head_dim, int rope, int rot_dim) {
 
 // Forming the heads saves a launch, about 3 us of the host's time. On the GPU, with the rotation in
 // front, against the head kernel behind: 4096 -> 6144 with 1 token 9.9 us against 11.2, 16 tokens 11.9
-// against 13.8, 32 tokens 13.2 against 15.6, 64 tokens 14.3 against 15.4; 1920 -> 5760 with 24 tokens
-// 11.5 against 11.3, 128 tokens 16.9 against 15.5.
+// against 13.8, 32 tokens 13.0 against 15.6, 64 tokens 14.0 against 15.4; 1920 -> 5760 with 24 tokens
+// 11.5 against 11.3, 128 tokens 16.4 against 15.5.
 bool gemm_w8_forms_heads(int64_t T, int head_dim, int rope, int rot_dim) {
   if (T <= kHeadRowTokens) return head_dim <= 128;    // a cluster of at most eight blocks
   if (T <= kSplitTokens) return PM % head_dim == 0;   // whole heads in a cluster's channels
