@@ -258,3 +258,25 @@ def test_an_attention_input_against_the_oracle(B, S, bits):
         z[:, lo:hi] = np.stack([c.real, c.imag], -1).reshape(a.shape)
     assert rel_fro(y.float().cpu().numpy(), z.reshape(T, N)) <= OUT_TOL
     plan.close()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_no_sequences(bits):
+    # an empty batch gives an empty result, with and without positions
+    oq = _oq()
+    d, D = 256, 32
+    plan = oq.Plan(d, 256, 1)
+    prep = (oq.prepare_weights_w8 if bits == 8 else oq.prepare_weights)(
+        plan, to_torch_bf16(synth.make_w(128, d)))
+    cos, sin = _tables(16, D)
+    h = oq.Heads(D, 2, 1, rope="halves", cos=cos, sin=sin)
+    x = torch.empty((0, d), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros((0, 5), dtype=torch.int32, device="cuda")
+    for kw in ({}, {"positions": pos}, {"batch": 0}, {"batch": 3}, {"batch": 0, "positions": pos}):
+        assert oq.linear_qkv(plan, h, x, *prep, **kw).shape == (0, 128)
+    with pytest.raises(oq.OQError):
+        oq.linear_qkv(plan, h, x.new_zeros((5, d)), *prep, positions=pos)
+    with pytest.raises(oq.OQError):
+        oq.linear_qkv(plan, h, x, *prep, batch=-1)
+    _ok(oq)
+    plan.close()

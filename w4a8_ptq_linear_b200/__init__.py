@@ -720,9 +720,9 @@ def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None
         raise OQError(OQ_ERR_INVALID_ARG, f"w: {Kw} columns for plan d={plan.d}")
     if positions is not None and positions.dim() == 2:
         batch = positions.shape[0]
-    if batch < 1 or T % batch:
+    if batch < 0 or (T % batch if batch else T):
         raise OQError(OQ_ERR_INVALID_ARG, f"{T} tokens are not {batch} sequences of one length")
-    S = T // batch
+    S = T // batch if batch else 0 if positions is None else positions.shape[-1]
     pos, pbs = _positions(positions, batch, S, dev)
     if out is None:
         out = x.new_empty((T, N))
