@@ -17,6 +17,7 @@
 
 #include "oq_internal.h"
 #include "ptx.cuh"
+#include "split_shape.h"
 
 namespace oq {
 
@@ -1079,19 +1080,15 @@ oq_status run_rows(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 // 40 x 4096 x 4096 9.5 us, 128 x 4096 x 12288 18.7, 256 x 12288 x 4096 21.8; a CTA's start, the barriers
 // and the end are 6 to 10 us of that, a K block 0.36 us.
 constexpr int PT = 256;                    // threads
-constexpr int PM = 128;                    // channels of a cluster
+constexpr int PM = kSplitChannels;         // channels of a cluster
 constexpr int PWB = PM * 128;              // weight bytes of a K block
 constexpr int kSplitTokens = kGemmW8FewTokens;   // tokens at most
-constexpr int kSplitMax = 8;               // CTAs of a cluster at most (portable size)
-constexpr int kRingMax = 12;               // stages at most
+static_assert(kSplitTail == 256 + 12 * kSplitTokens, "barriers, scales, means, positions");
 
 struct SplitParams {
   W8Params w;
   TileHeads h;                             // heads formed in the epilogue (HEADS)
-  int npad;                                // tokens, rounded up to 16 (the MMA's N)
-  int tcols;                               // TMEM columns: a power of two >= 32
-  int ks, nkb, ns;                         // K blocks of a CTA, in all; stages
-  int off_bar;                             // ring and partial sums lie in front of the barriers
+  int npad, tcols, ks, nkb, ns, off_bar;   // of SplitShape
 };
 
 // Heads of D elements, D a divisor of 128, in the epilogue of the split: a lane holds four channels (o
@@ -1393,9 +1390,10 @@ __global__ void __launch_bounds__(PT)
   }
 }
 
-// How a product is split, and what it is expected to take (see choose_shape).
+// How a product is split, and what it is expected to take (see "which shape" below).
 struct SplitPlan {
-  int S = 0, ks = 0, ns = 0, off_bar = 0, smem = 0;
+  int S = 0;
+  SplitShape shape;
   double us = 1e30;
 };
 
@@ -1417,27 +1415,20 @@ SplitPlan plan_split(const W8Params& w) {
   for (int S = 1; S <= kSplitMax; ++S) {
     SplitPlan c;
     c.S = S;
-    c.ks = (nkb + S - 1) / S;
-    if ((S - 1) * c.ks >= nkb) continue;   // a CTA would have nothing to do
-    // ring: as deep as the CTA has blocks, within half an SM's shared memory where the partial sums
-    // leave room for two CTAs, else within all of it; at least as large as the partial sums
-    const int stage = PWB + npad * 128;
-    const int room = npad <= 192 ? 108 * 1024 : 216 * 1024;
-    c.ns = std::min(std::min(c.ks, kRingMax), room / stage);
-    c.off_bar = (std::max(c.ns * stage, npad * PM * 4) + 1023) / 1024 * 1024;
-    c.smem = c.off_bar + 256 + 12 * kSplitTokens + 1024;
-    if (resident_clusters(kern, S, c.smem, PT) <= 0) continue;   // does not launch here
+    c.shape = split_shape(w.T, w.K, S);
+    if (c.shape.ks == 0) continue;   // a CTA would have nothing to do
+    if (resident_clusters(kern, S, c.shape.smem, PT) <= 0) continue;   // does not launch here
     // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
     // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
     // occupancy query counts one CTA to an SM; 192 CTAs in pairs ran faster than 96 alone).
-    const double slots = (c.smem <= 112 * 1024 ? 2 : 1) * sms;
+    const double slots = split_ctas_per_sm(c.shape.smem) * sms;
     const int fit = std::max(1, (int)(S == 1 ? slots : 0.9 * slots / S));
     // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
     // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters that
     // does not fit waits for the one before)
     const int waves = (tiles + fit - 1) / fit;
     const double share = std::max(1.0, std::min(tiles, fit) * S / sms);
-    c.us = waves * (5.6 + 0.02 * npad + share * c.ks * (0.36 + 0.0004 * npad) + 0.2 * S);
+    c.us = waves * (5.6 + 0.02 * npad + share * c.shape.ks * (0.36 + 0.0004 * npad) + 0.2 * S);
     if (c.us < best.us) best = c;
   }
   std::lock_guard<std::mutex> lock(mu);
@@ -1450,13 +1441,8 @@ oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* he
   SplitParams p{};
   p.w = w;
   if (heads) p.h = head_params(*heads);
-  p.npad = (w.T + 15) / 16 * 16;
-  p.tcols = 32;
-  while (p.tcols < p.npad) p.tcols *= 2;
-  p.nkb = (w.K + 127) / 128;
-  p.ks = plan.ks;
-  p.ns = plan.ns;
-  p.off_bar = plan.off_bar;
+  const SplitShape& c = plan.shape;
+  p.npad = c.npad; p.tcols = c.tcols; p.nkb = c.nkb; p.ks = c.ks; p.ns = c.ns; p.off_bar = c.off_bar;
   CUtensorMap tw, ta;
   const uint64_t K = (uint64_t)w.K, N = (uint64_t)w.N, T = (uint64_t)w.T;
   if (!tma_map_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.w, K, N, K, 128, PM,
@@ -1468,7 +1454,7 @@ oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* he
   const auto kern = heads ? &k_gemm_w8_split<true> : &k_gemm_w8_split<false>;
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8_split)");
-  e = launch_beside(kern, (unsigned)(tiles * plan.S), PT, (size_t)plan.smem, (unsigned)plan.S,
+  e = launch_beside(kern, (unsigned)(tiles * plan.S), PT, (size_t)c.smem, (unsigned)plan.S,
                     w.dependent, s, tw, ta, p);
   return e == cudaSuccess ? OQ_OK : cuda_fail(e, "launch gemm_w8_split");
 }
