@@ -26,7 +26,6 @@ int main() {
           std::printf("%d %d %d %d %d %d %d %d %d\n", T, K, S, c.npad, c.tcols, c.ks, c.ns, c.off_bar,
                       c.smem);
       }
-  std::printf("%d %d\n", oq::split_ctas_per_sm(115712), oq::split_ctas_per_sm(115713));
 }
 """
 
@@ -39,9 +38,8 @@ def shapes(tmp_path_factory):
         f.write(PROGRAM)
     subprocess.run(["g++", "-std=c++17", "-O1", "-I", CSRC, src, "-o", exe], check=True)
     lines = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.splitlines()
-    assert lines[-1] == "2 1"   # two blocks of (228 KB / 2 - 1 KB)
     return sorted({tuple(map(int, l.split()))[3:] + (int(l.split()[1]), int(l.split()[2]))
-                   for l in lines[:-1]})
+                   for l in lines})
 
 
 def test_no_mix_of_ctas_asks_for_more_tensor_memory_than_an_sm_has(shapes):

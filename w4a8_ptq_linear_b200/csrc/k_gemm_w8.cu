@@ -1421,7 +1421,7 @@ SplitPlan plan_split(const W8Params& w) {
     // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
     // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
     // occupancy query counts one CTA to an SM; 192 CTAs in pairs ran faster than 96 alone).
-    const double slots = split_ctas_per_sm(c.shape.smem) * sms;
+    const double slots = split_ctas_per_sm(c.shape) * sms;
     const int fit = std::max(1, (int)(S == 1 ? slots : 0.9 * slots / S));
     // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
     // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters that

@@ -14,9 +14,6 @@ constexpr int kSmemOfSm = 228 * 1024;      // shared memory of an SM,
 constexpr int kSmemOfBlock = 1024;         // of which every block takes this much for itself
 constexpr int kTmemOfSm = 512;             // tensor memory columns of an SM
 
-// CTAs of `smem` bytes that an SM holds, two at most (more are not counted on)
-inline int split_ctas_per_sm(int smem) { return 2 * (smem + kSmemOfBlock) <= kSmemOfSm ? 2 : 1; }
-
 struct SplitShape {
   int npad = 0;      // tokens, rounded up to 16 (the MMA's columns)
   int tcols = 0;     // TMEM columns: a power of two >= 32
@@ -24,8 +21,13 @@ struct SplitShape {
   int ks = 0;        // of one CTA,
   int ns = 0;        // and stages of its ring
   int off_bar = 0;   // ring and partial sums lie in front of the barriers
-  int smem = 0;
+  int need = 0;      // shared memory that is used,
+  int smem = 0;      // and asked for
 };
+
+// CTAs to an SM that the estimate of a split's time counts on: two within 112 KB each. (With the few
+// KB more that an SM has, 16 x 4096 x 12288 was split, 14.4 us, where rows take 13.7.)
+inline int split_ctas_per_sm(const SplitShape& c) { return c.need <= 112 * 1024 ? 2 : 1; }
 
 // T tokens, K bytes of K, over S CTAs; ks = 0 where a CTA would have nothing to do.
 //
@@ -51,8 +53,8 @@ inline SplitShape split_shape(int T, int K, int S) {
   c.ks = ks;
   c.ns = std::min(std::min(ks, kRingMax), room / stage);
   c.off_bar = (std::max(c.ns * stage, c.npad * kSplitChannels * 4) + 1023) / 1024 * 1024;
-  c.smem = std::max(c.off_bar + kSplitTail + 1024,   // 1024: the base is aligned in the kernel
-                    c.tcols * (kSmemOfSm / kTmemOfSm) - kSmemOfBlock);
+  c.need = c.off_bar + kSplitTail + 1024;   // 1024: the base is aligned in the kernel
+  c.smem = std::max(c.need, c.tcols * (kSmemOfSm / kTmemOfSm) - kSmemOfBlock);
   return c;
 }
 
