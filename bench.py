@@ -61,7 +61,7 @@ NCU_TRAFFIC = {
     # that it reads a fraction of the weights (profiles/k_linear_fused_t256.md)
     # dram__bytes_read.sum, dram__bytes_write.sum of the split-K GEMM k_linear_fused<0, 1, 0, 0> at T = 256
     # (profiles/k_gemm_splitk_t256.md): dram read 5.558 MB + write 0
-    ("dit_w4a8@T256", "k_gemm"): {"sha": "8d5c5d5381a3e22bfb7dd801e3c23b1639653c392cdaf29e5f574263b7ab32a9", "bytes": 5558272, "sources": "k_linear_fused"},
+    ("dit_w4a8@T256", "k_gemm"): {"sha": "ea8285ebd297d221c8ffcad5ac8207871b8cc7b363e4bd478dfd050f59a8b81d", "bytes": 5558272, "sources": "k_linear_fused"},
 }
 
 

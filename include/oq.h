@@ -126,7 +126,8 @@ const char* oq_last_error(void);
 
 /* Synchronizes the current device, then returns OQ_ERR_DEVICE_TIMEOUT if a kernel recorded
  * a bounded-wait failure since the last clear (its site code in *code_out if non-NULL),
- * OQ_ERR_CUDA if the device reports an error, else OQ_OK. clear != 0 resets the word. */
+ * OQ_ERR_CUDA if the device reports an error or a single launch (oq_linear_fused, oq_linear) ran
+ * without its cluster (ncu replays it so: that kernel then computes nothing), else OQ_OK. clear != 0 resets the word. */
 oq_status oq_device_status(int clear, uint64_t* code_out);
 
 /* ---- policies (host only) ---------------------------------------------------------- */
@@ -527,6 +528,11 @@ oq_status oq_debug_pair_layout(int d, int h, uint64_t seed, int32_t* word_host);
  * will arrive on, for at most timeout_ns, then records a timeout and returns. The next
  * oq_device_status() reports OQ_ERR_DEVICE_TIMEOUT. The GPU stays usable. */
 oq_status oq_debug_wait_timeout(uint64_t timeout_ns, void* stream);
+
+/* Test hook for a single launch (oq_linear_fused, oq_linear) that loses its cluster, as under a
+ * profiler that replays cooperative launches without it: the calling thread's next one goes out so.
+ * Its kernel computes nothing, and the next oq_device_status() reports OQ_ERR_CUDA. */
+oq_status oq_debug_drop_cluster(void);
 
 #ifdef __cplusplus
 }

@@ -71,6 +71,7 @@ SIGNATURES = [
                            _P, _SZ, _P]),
     ("oq_mma_peak_loop", _I, [_I, _I64, _P, _P]),
     ("oq_debug_pair_layout", _I, [_I, _I, _U64, _P]),
+    ("oq_debug_drop_cluster", _I, []),
 ]
 
 
@@ -760,3 +761,8 @@ def debug_pair_layout(d: int, h: int, seed: int = 0):
 def debug_wait_timeout(timeout_ns: int, stream=None):
     """Launch a kernel whose bounded wait must give up (tests the error path)."""
     _check(lib().oq_debug_wait_timeout(timeout_ns, _stream(stream)))
+
+
+def debug_drop_cluster():
+    """oq_debug_drop_cluster: this thread's next single launch goes out without its cluster."""
+    _check(lib().oq_debug_drop_cluster())

@@ -69,7 +69,7 @@ struct FusedParams {
   const float* w_rowsum;          // null without centering
   const __nv_bfloat16* bias;      // may be null
   __nv_bfloat16* y;               // [T, N]
-  int T, K, N, npad, ks, nkb, ns, rq_threads;
+  int T, K, N, npad, S, ks, nkb, ns, rq_threads;
   int off_u, off_bar, off_tok;    // shared-memory offsets: union region, barriers, token scales
   unsigned long long* err;
   unsigned long long limit_ns;
@@ -144,6 +144,12 @@ __global__ void __launch_bounds__(FT, 1)
   const uint32_t wfull = dev::smem_u32(&bars[2 * kFusedMaxNs + 1]);
   const int stage_bytes = npad * 128;
 
+  // The launch lost its cluster: a profiler that replays cooperative launches (ncu) does so without
+  // it, and every CTA would take its own K blocks for all of K. The whole grid leaves.
+  if (S != p.S) {
+    if (tid == 0) dev::report(p.err, kSiteFusedCluster);
+    return;
+  }
   if (tid == 0) {
     for (int st = 0; st < ns; ++st) {
       dev::mbar_init(full(st), 1);
@@ -474,6 +480,7 @@ oq_status launch_shaped(const void* fn, bool cooperative, FusedParams& p, const 
   p.K = (int)K;
   p.N = (int)N;
   p.npad = npad;
+  p.S = f.S;
   p.ks = f.ks;
   p.ns = f.ns;
   p.nkb = nkb;
@@ -490,14 +497,21 @@ oq_status launch_shaped(const void* fn, bool cooperative, FusedParams& p, const 
   cfg.dynamicSmemBytes = f.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)f.S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
+  unsigned n = 0;
+  if (!(cooperative && take_drop_cluster())) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)f.S;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (cooperative) {
+    attr[n].id = cudaLaunchAttributeCooperative;
+    attr[n].val.cooperative = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = cooperative ? 2 : 1;
+  cfg.numAttrs = n;
   void* args[] = {&tx, &tw, &p};
   ce = cudaLaunchKernelExC(&cfg, fn, args);
   if (ce == cudaErrorCooperativeLaunchTooLarge) {

@@ -32,6 +32,14 @@ oq_status cuda_fail(cudaError_t e, const char* what) {
   return fail(OQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+static thread_local bool g_drop_cluster = false;
+
+bool take_drop_cluster() {
+  const bool drop = g_drop_cluster;
+  g_drop_cluster = false;
+  return drop;
+}
+
 unsigned long long* device_error_word() {
   constexpr int kMaxDev = 64;
   static unsigned long long* ptrs[kMaxDev] = {};
@@ -233,6 +241,8 @@ oq_status oq_device_status(int clear, uint64_t* code_out) {
   if (v && site >= kSiteBounds)
     return fail(OQ_ERR_INVALID_ARG, "index out of range (checked build): site %#x block %u", site,
                 (unsigned)(v & 0xFFFFFFFFu));
+  if (site == kSiteFusedCluster)
+    return fail(OQ_ERR_CUDA, "single-launch layer: launched without its cluster (under a profiler?)");
   if (v) return fail(OQ_ERR_DEVICE_TIMEOUT, "device wait gave up: site %u block %u", site,
                      (unsigned)(v & 0xFFFFFFFFu));
   return OQ_OK;
@@ -1015,6 +1025,11 @@ oq_status oq_debug_wait_timeout(uint64_t timeout_ns, void* stream) {
   k_debug_wait<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(w, timeout_ns);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch debug wait");
+  return OQ_OK;
+}
+
+oq_status oq_debug_drop_cluster(void) {
+  g_drop_cluster = true;
   return OQ_OK;
 }
 

@@ -69,6 +69,7 @@ enum : uint32_t {
   kSitePeak = 21,          // tensor-core peak loop: completion of the MMAs
   kSiteFusedLoad = 22,     // single-launch layer: activation codes loaded
   kSiteFusedMma = 23,      // single-launch layer: partial sums complete
+  kSiteFusedCluster = 24,  // single-launch layer: launched without its cluster (no wait gave up)
   kSiteDebug = 99,         // oq_debug_wait_timeout
   // checked builds (-DOQ_CHECKED): an index outside its buffer (sites >= kSiteBounds)
   kSiteBounds = 0x100,
@@ -156,6 +157,9 @@ struct FusedArgs {
   int64_t T = 0, K = 0, N = 0;
 };
 oq_status launch_linear_fused(const FusedArgs& a, cudaStream_t s);
+// Whether oq_debug_drop_cluster asked this host thread's next single launch to go without its
+// cluster (asked once).
+bool take_drop_cluster();
 // The same kernel's split-K GEMM alone (W4A8, bf16 output, 1 <= T <= 256) on codes a previous
 // launch wrote; OQ_ERR_UNSUPPORTED (nothing launched) outside that or when it does not fit.
 oq_status launch_gemm_splitk(const GemmArgs& g, cudaStream_t s);
