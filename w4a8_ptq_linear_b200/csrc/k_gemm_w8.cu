@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       s_head[3 * TN + i] = tp.h.kb ? tp.h.kb[i] : 0.f;
     }
   }
+  __syncwarp();   // the lanes' ways parted above; what follows is for whole warps
   if (warp == 1) {
     dev::tmem_alloc_pair(dev::smem_u32(&s_misc[0]), 2 * TN);
     dev::tmem_relinquish_pair();
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (!ready) give_up();
         s_misc[2 + b] = ready ? 1u : 0u;
       }
+      __syncwarp();
       dev::named_bar(1, NEPI);
       ok = *reinterpret_cast<volatile uint32_t*>(&s_misc[2 + b]) != 0;
       dev::tc_fence_after();
@@ -872,6 +874,7 @@ __device__ __forceinline__ void cluster_heads(const RowParams& rp, int o0, const
     }
     m[e] = 0.f;
   }
+  __syncwarp();   // the cluster's barrier is for whole warps, whose lanes parted at the stores
   dev::cluster_sync();
 #pragma unroll
   for (int e = 0; e < NO; ++e) {
@@ -887,6 +890,7 @@ __device__ __forceinline__ void cluster_heads(const RowParams& rp, int o0, const
       const float part = half_warp_sum((y[e] - m[e]) * (y[e] - m[e]));
       if (oc == 0 && t < MT) s_stat[1][t] = part;
     }
+    __syncwarp();
     dev::cluster_sync();
 #pragma unroll
     for (int e = 0; e < NO; ++e) {
