@@ -29,7 +29,7 @@ LIB_CHECKED = os.path.join(LIB_DIR, "liboq_checked.so")
 SOURCES = ["oq_api.cu", "k_rotate_quant.cu", "k_gemm.cu", "k_weights_g64.cu", "oq_plan.cpp",
            "oq_static_scratch.cu", "k_peak.cu", "k_linear_fused.cu", "k_gemm_w8.cu", "k_heads.cu",
            "k_rq_lead.cu"]
-HEADERS = ["oq_internal.h", "ptx.cuh", "rq_device.cuh", "split_shape.h"]
+HEADERS = ["oq_internal.h", "ptx.cuh", "rq_device.cuh", "split_shape.h", "kept.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -10,11 +10,10 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
 #include <new>
 #include <tuple>
 
+#include "kept.h"
 #include "oq_internal.h"
 #include "ptx.cuh"
 #include "split_shape.h"
@@ -647,33 +646,27 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
 }
 
-// Clusters that are resident at once, per device and launch shape (0 if the query fails).
+// Clusters that are resident at once, per device and launch shape (-1 if the query fails).
 int resident_clusters(const void* kern, int cluster, int smem, int threads) {
-  static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int, int>, int> kept;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple(dev, kern, cluster, smem);
-  auto found = kept.find(key);
-  if (found != kept.end()) return found->second;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(cluster * device_sms()));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+  static Kept<std::tuple<int, const void*, int, int>, int> kept;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  const bool known = kept.get(std::make_tuple(dev, kern, cluster, smem), &n, [&](int* clusters) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(cluster * device_sms()));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(clusters, kern, &cfg) == cudaSuccess) return true;
     cudaGetLastError();
-    n = 0;
-  }
-  kept[key] = n;
-  return n;
+    return false;
+  });
+  return known ? n : -1;
 }
 
 // Launch with an optional cluster, beside the launch before where `dependent`.
@@ -729,7 +722,8 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
   cudaError_t e = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(gemm_w8)");
   int units = resident_clusters(reinterpret_cast<const void*>(kern), 2, SMEM, NTHR);
-  if (units <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no CTA pair fits on this device");
+  if (units < 0) return fail(OQ_ERR_CUDA, "gemm_w8: the occupancy query failed");
+  if (units == 0) return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no CTA pair fits on this device");
   TileParams p{};
   p.w = w;
   p.cw = CH;
@@ -1404,40 +1398,37 @@ struct SplitPlan {
 SplitPlan plan_split(const W8Params& w) {
   const int npad = (w.T + 15) / 16 * 16, nkb = (w.K + 127) / 128, tiles = (w.N + PM - 1) / PM;
   const void* kern = reinterpret_cast<const void*>(&k_gemm_w8_split<false>);
-  static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int>, SplitPlan> kept;
-  SplitPlan best;
+  static Kept<std::tuple<int, int, int, int>, SplitPlan> kept;
+  SplitPlan plan;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || allow_max_dynamic_smem(kern) != cudaSuccess) return best;
-  const auto key = std::make_tuple(dev, npad, nkb, tiles);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    auto found = kept.find(key);
-    if (found != kept.end()) return found->second;
-  }
-  const double sms = device_sms();
-  for (int S = 1; S <= kSplitMax; ++S) {
-    SplitPlan c;
-    c.S = S;
-    c.shape = split_shape(w.T, w.K, S);
-    if (c.shape.ks == 0) continue;   // a CTA would have nothing to do
-    if (resident_clusters(kern, S, c.shape.smem, PT) <= 0) continue;   // does not launch here
-    // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
-    // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
-    // occupancy query counts one CTA to an SM; 192 CTAs in pairs ran faster than 96 alone).
-    const double slots = split_ctas_per_sm(c.shape) * sms;
-    const int fit = std::max(1, (int)(S == 1 ? slots : 0.9 * slots / S));
-    // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
-    // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters that
-    // does not fit waits for the one before)
-    const int waves = (tiles + fit - 1) / fit;
-    const double share = std::max(1.0, std::min(tiles, fit) * S / sms);
-    c.us = waves * (5.6 + 0.02 * npad + share * c.shape.ks * (0.36 + 0.0004 * npad) + 0.2 * S);
-    if (c.us < best.us) best = c;
-  }
-  std::lock_guard<std::mutex> lock(mu);
-  kept[key] = best;
-  return best;
+  if (cudaGetDevice(&dev) != cudaSuccess || allow_max_dynamic_smem(kern) != cudaSuccess) return plan;
+  kept.get(std::make_tuple(dev, npad, nkb, tiles), &plan, [&](SplitPlan* best) {
+    const double sms = device_sms();
+    bool known = true;
+    for (int S = 1; S <= kSplitMax; ++S) {
+      SplitPlan c;
+      c.S = S;
+      c.shape = split_shape(w.T, w.K, S);
+      if (c.shape.ks == 0) continue;   // a CTA would have nothing to do
+      const int resident = resident_clusters(kern, S, c.shape.smem, PT);
+      known = known && resident >= 0;
+      if (resident <= 0) continue;     // does not launch here, or could not be asked now
+      // Clusters that run at once: two CTAs to an SM where their shared memory allows, and about a
+      // tenth less than the SMs would hold where a cluster's CTAs have to find room together (the
+      // occupancy query counts one CTA to an SM; 192 CTAs in pairs ran faster than 96 alone).
+      const double slots = split_ctas_per_sm(c.shape) * sms;
+      const int fit = std::max(1, (int)(S == 1 ? slots : 0.9 * slots / S));
+      // Fitted to measurements (one block of K of a CTA: 0.36 us and more with the tokens; two CTAs
+      // on an SM share its rate; a CTA's start and end: 5.6 us and 0.02 a token; a wave of clusters
+      // that does not fit waits for the one before)
+      const int waves = (tiles + fit - 1) / fit;
+      const double share = std::max(1.0, std::min(tiles, fit) * S / sms);
+      c.us = waves * (5.6 + 0.02 * npad + share * c.shape.ks * (0.36 + 0.0004 * npad) + 0.2 * S);
+      if (c.us < best->us) *best = c;
+    }
+    return known;
+  });
+  return plan;
 }
 
 oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* heads,
