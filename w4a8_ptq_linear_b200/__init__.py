@@ -8,6 +8,11 @@ call raises ``OQError``.
 
 The function names follow the C ABI: ``rotate_quantize``, ``prepare_weights``,
 ``gemm_w4a8``, ``gemm_w4a4``, ``gemm_w4a2``, ``linear`` (oq_rotate_quantize, oq_prepare_weights, ...).
+
+``stream=`` runs a call on another stream than the current one. What the call allocates (results,
+workspace) then belongs to that stream; as ever in torch, the caller orders the streams: the call's
+stream behind whatever wrote its inputs, and other streams behind the call before they read its
+results (``wait_stream``), with ``record_stream`` for a tensor that outlives its owner's stream.
 """
 from __future__ import annotations
 
@@ -145,6 +150,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(like, shape, dtype, stream):
+    """A new tensor on like's device, from the allocator's pool of the stream that the call runs on:
+    a block of another stream's pool may still be in use there, and would go back to that stream
+    while this one writes it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def device_status(clear: bool = True):
     """(status, code) of the device error word; synchronizes the current device."""
     code = ctypes.c_uint64(0)
@@ -266,16 +282,14 @@ def rotate_quantize(plan: Plan, x, *, codes=None, scale=None, mean=None, rotated
     Returns (codes, scale, mean or None, rotated float32 [T, d] or None)."""
     import torch
     T, ldx = x.shape[0], x.stride(0)
-    dev = x.device
     if codes is None:
-        codes = torch.empty((T, plan.code_row_bytes),
-                            dtype=torch.int8 if plan.act == "int8_absmax" else torch.uint8,
-                            device=dev)
+        codes = _new(x, (T, plan.code_row_bytes),
+                     torch.int8 if plan.act == "int8_absmax" else torch.uint8, stream)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=dev)
+        scale = _new(x, (T,), torch.float32, stream)
     if plan.center and mean is None:
-        mean = torch.empty(T, dtype=torch.float32, device=dev)
-    rot = torch.empty((T, plan.d), dtype=torch.float32, device=dev) if rotated else None
+        mean = _new(x, (T,), torch.float32, stream)
+    rot = _new(x, (T, plan.d), torch.float32, stream) if rotated else None
     _check(lib().oq_rotate_quantize(plan.handle, _ptr(x), T, ldx, _ptr(codes), _ptr(scale),
                                     _ptr(mean) if plan.center else None, _ptr(rot),
                                     _stream(stream)))
@@ -286,20 +300,19 @@ def prepare_weights(plan: Plan, w, *, stream=None):
     """oq_prepare_weights on a bf16 [n_out, d] CUDA tensor: (w_packed, w_scale, w_rowsum)."""
     import torch
     n = w.shape[0]
-    wp = torch.empty((n, plan.d // 2), dtype=torch.uint8, device=w.device)
-    ws = torch.empty(n, dtype=torch.float32, device=w.device)
-    w1 = torch.empty(n, dtype=torch.float32, device=w.device)
+    wp = _new(w, (n, plan.d // 2), torch.uint8, stream)
+    ws = _new(w, (n,), torch.float32, stream)
+    w1 = _new(w, (n,), torch.float32, stream)
     _check(lib().oq_prepare_weights(plan.handle, _ptr(w), n, w.stride(0), _ptr(wp), _ptr(ws),
                                     _ptr(w1), _stream(stream)))
     return wp, ws, w1
 
 
-def _out(T, N, out_kind, acc_dtype, dev, out):
+def _out(like, T, N, out_kind, acc_dtype, out, stream):
     import torch
     if out is not None:
         return out
-    dt = torch.bfloat16 if out_kind == OUT_BF16 else acc_dtype
-    return torch.empty((T, N), dtype=dt, device=dev)
+    return _new(like, (T, N), torch.bfloat16 if out_kind == OUT_BF16 else acc_dtype, stream)
 
 
 def gemm_w4a8(a, a_scale, w_packed, w_scale, *, mean=None, w_rowsum=None, bias=None,
@@ -308,7 +321,7 @@ def gemm_w4a8(a, a_scale, w_packed, w_scale, *, mean=None, w_rowsum=None, bias=N
     import torch
     T, K = a.shape
     N = w_packed.shape[0]
-    out = _out(T, N, out_kind, torch.int32, a.device, out)
+    out = _out(a, T, N, out_kind, torch.int32, out, stream)
     _check(lib().oq_gemm_w4a8(_ptr(a), _ptr(a_scale), _ptr(mean), _ptr(w_packed), _ptr(w_scale),
                               _ptr(w_rowsum), _ptr(bias), T, K, N, out_kind, _ptr(out),
                               _stream(stream)))
@@ -322,7 +335,7 @@ def gemm_w4a4(plan, kind, a_packed, a_scale, w_packed, w_scale, *, mean=None, w_
     T, K = a_packed.shape[0], a_packed.shape[1] * 2
     N = w_packed.shape[0]
     acc_dt = torch.float32 if kind.startswith("int4_lloydmax") else torch.int32
-    out = _out(T, N, out_kind, acc_dt, a_packed.device, out)
+    out = _out(a_packed, T, N, out_kind, acc_dt, out, stream)
     _check(lib().oq_gemm_w4a4(plan.handle if plan is not None else None, ACT_KINDS[kind],
                               _ptr(a_packed), _ptr(a_scale), _ptr(mean), _ptr(w_packed),
                               _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), T, K, N, out_kind,
@@ -336,7 +349,7 @@ def gemm_w4a2(a_packed, a_scale, w_packed, w_scale, *, mean=None, w_rowsum=None,
     import torch
     T, K = a_packed.shape[0], a_packed.shape[1] * 4
     N = w_packed.shape[0]
-    out = _out(T, N, out_kind, torch.int32, a_packed.device, out)
+    out = _out(a_packed, T, N, out_kind, torch.int32, out, stream)
     _check(lib().oq_gemm_w4a2(_ptr(a_packed), _ptr(a_scale), _ptr(mean), _ptr(w_packed),
                               _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), T, K, N, out_kind,
                               _ptr(out), _stream(stream)))
@@ -349,7 +362,7 @@ def gemm_w4a8_lloydmax(plan, codes, sigma, w_packed, w_scale, *, mean=None, w_ro
     import torch
     T, K = codes.shape
     N = w_packed.shape[0]
-    out = _out(T, N, out_kind, torch.float32, codes.device, out)
+    out = _out(codes, T, N, out_kind, torch.float32, out, stream)
     _check(lib().oq_gemm_w4a8_lloydmax(plan.handle, _ptr(codes), _ptr(sigma), _ptr(mean),
                                        _ptr(w_packed), _ptr(w_scale), _ptr(w_rowsum), _ptr(bias),
                                        T, K, N, out_kind, _ptr(out), _stream(stream)))
@@ -364,9 +377,9 @@ def linear(plan: Plan, x, w_packed, w_scale, w_rowsum=None, bias=None, *, worksp
     N = w_packed.shape[0]
     need = plan.workspace_bytes(T)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _new(x, (max(need, 256),), torch.uint8, stream)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(x, (T, N), torch.bfloat16, stream)
     _check(lib().oq_linear(plan.handle, _ptr(x), T, x.stride(0), _ptr(w_packed), _ptr(w_scale),
                            _ptr(w_rowsum), _ptr(bias), N, _ptr(out), _ptr(workspace),
                            workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -382,9 +395,9 @@ def linear_fused(plan: Plan, x, w_packed, w_scale, w_rowsum=None, bias=None, *, 
     N = w_packed.shape[0]
     need = plan.workspace_bytes(T)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _new(x, (max(need, 256),), torch.uint8, stream)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(x, (T, N), torch.bfloat16, stream)
     _check(lib().oq_linear_fused(plan.handle, _ptr(x), T, x.stride(0), _ptr(w_packed),
                                  _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), N, _ptr(out),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -400,10 +413,10 @@ def prepare_weights_g64(plan: Plan, w, *, stream=None):
     [n] (ones); w_rowsum float32 [n])."""
     import torch
     n = w.shape[0]
-    wp = torch.empty((n, plan.d // 2), dtype=torch.uint8, device=w.device)
-    wsz = torch.empty((plan.d // 64, n), dtype=torch.int32, device=w.device)
-    ws = torch.empty(n, dtype=torch.float32, device=w.device)
-    w1 = torch.empty(n, dtype=torch.float32, device=w.device)
+    wp = _new(w, (n, plan.d // 2), torch.uint8, stream)
+    wsz = _new(w, (plan.d // 64, n), torch.int32, stream)
+    ws = _new(w, (n,), torch.float32, stream)
+    w1 = _new(w, (n,), torch.float32, stream)
     _check(lib().oq_prepare_weights_g64(plan.handle, _ptr(w), n, w.stride(0), _ptr(wp), _ptr(wsz),
                                         _ptr(ws), _ptr(w1), _stream(stream)))
     return wp, wsz, ws, w1
@@ -415,7 +428,7 @@ def gemm_w4a4_g64(kind, a_packed, a_scale, w_packed, w_sz, w_scale, *, mean=None
     import torch
     T, K = a_packed.shape[0], a_packed.shape[1] * 2
     N = w_packed.shape[0]
-    out = _out(T, N, out_kind, torch.float32, a_packed.device, out)
+    out = _out(a_packed, T, N, out_kind, torch.float32, out, stream)
     _check(lib().oq_gemm_w4a4_g64(ACT_KINDS[kind], _ptr(a_packed), _ptr(a_scale), _ptr(mean),
                                   _ptr(w_packed), _ptr(w_sz), _ptr(w_scale), _ptr(w_rowsum),
                                   _ptr(bias), T, K, N, out_kind, _ptr(out), _stream(stream)))
@@ -430,9 +443,9 @@ def linear_g64(plan: Plan, x, w_packed, w_sz, w_scale, w_rowsum=None, bias=None,
     N = w_packed.shape[0]
     need = plan.workspace_bytes(T)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _new(x, (max(need, 256),), torch.uint8, stream)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(x, (T, N), torch.bfloat16, stream)
     _check(lib().oq_linear_g64(plan.handle, _ptr(x), T, x.stride(0), _ptr(w_packed), _ptr(w_sz),
                                _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), N, _ptr(out),
                                _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -453,7 +466,7 @@ def linear_static_scratch(plan: Plan, x, w_packed, w_scale, w_rowsum=None, bias=
     T = x.shape[0]
     N = w_packed.shape[0]
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(x, (T, N), torch.bfloat16, stream)
     _check(lib().oq_linear_static_scratch(plan.handle, _ptr(x), T, x.stride(0), _ptr(w_packed),
                                           _ptr(w_scale), _ptr(w_rowsum), _ptr(bias), N,
                                           _ptr(out), _stream(stream)))
@@ -529,13 +542,11 @@ def _layer_bytes(plan, T):
 
 
 def _scratch(workspace, need, like, stream):
-    """Pointer and size of the caller's workspace, or of one from torch's allocator that stays
-    in use on `stream`; the tensor itself, to be kept until the call has been made."""
+    """Pointer and size of the caller's workspace, or of one from torch's allocator; the tensor
+    itself, to be kept until the call has been made."""
     import torch
     if workspace is None:
-        workspace = like.new_empty(max(need, 256), dtype=torch.uint8)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _new(like, (max(need, 256),), torch.uint8, stream)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise OQError(OQ_ERR_INVALID_ARG, "workspace: must be contiguous, on the input's device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -547,9 +558,9 @@ def prepare_weights_w8(plan: Plan, w, *, stream=None):
     import torch
     dev = _device()
     wp, n, ldw = _need_rows(w, "w", torch.bfloat16, plan.d, dev)
-    codes = torch.empty((n, plan.d), dtype=torch.int8, device=w.device)
-    ws = torch.empty(n, dtype=torch.float32, device=w.device)
-    w1 = torch.empty(n, dtype=torch.float32, device=w.device)
+    codes = _new(w, (n, plan.d), torch.int8, stream)
+    ws = _new(w, (n,), torch.float32, stream)
+    w1 = _new(w, (n,), torch.float32, stream)
     _check(lib().oq_prepare_weights_w8(plan.handle, wp, n, ldw, codes.data_ptr(), ws.data_ptr(),
                                        w1.data_ptr(), _raw_stream(stream, dev)))
     return codes, ws, w1
@@ -566,7 +577,7 @@ def gemm_w8a8(a, a_scale, w_codes, w_scale, *, mean=None, w_rowsum=None, bias=No
         raise OQError(OQ_ERR_INVALID_ARG, f"a has {K} columns, w_codes {Kw}")
     dt = torch.bfloat16 if out_kind == OUT_BF16 else torch.int32
     if out is None:
-        out = a.new_empty((T, N), dtype=dt)
+        out = _new(a, (T, N), dt, stream)
     else:
         _need(out, "out", dt, (T, N), dev)
     _check(lib().oq_gemm_w8a8(
@@ -587,7 +598,7 @@ def linear_w8a8(plan: Plan, x, w_codes, w_scale, w_rowsum=None, bias=None, *, wo
     if Kw != plan.d:
         raise OQError(OQ_ERR_INVALID_ARG, f"w_codes: {Kw} columns, plan d={plan.d}")
     if out is None:
-        out = x.new_empty((T, N))
+        out = _new(x, (T, N), bf16, stream)
     else:
         _need(out, "out", bf16, (T, N), dev)
     ws, nbytes, keep = _scratch(workspace, _layer_bytes(plan, T), x, stream)
@@ -690,7 +701,7 @@ def qk_norm_rope(heads: Heads, q, k, *, positions=None, q_out=None, k_out=None, 
         shape = (*lead, n, D)
         ptr, st = _head_rows(t, name, shape, dev)
         if o is None:
-            o = t.new_empty(shape)
+            o = _new(t, shape, torch.bfloat16, stream)
             optr, ost = o.data_ptr(), (lead[-1] * n * D, n * D, D)
         else:
             optr, ost = _head_rows(o, name + "_out", shape, dev)
@@ -726,7 +737,7 @@ def linear_qkv(plan: Plan, heads: Heads, x, w, w_scale, w_rowsum=None, bias=None
     S = T // batch if batch else 0 if positions is None else positions.shape[-1]
     pos, pbs = _positions(positions, batch, S, dev)
     if out is None:
-        out = x.new_empty((T, N))
+        out = _new(x, (T, N), bf16, stream)
     else:
         _need(out, "out", bf16, (T, N), dev)
     L, kind = lib(), W_INT8 if w8 else W_INT4
