@@ -532,11 +532,16 @@ def _need_2d(t, name, dtype, dev):
     return t.data_ptr(), *t.shape
 
 
+_LAYER_SIZES = 64   # numbers of tokens whose workspace size a plan remembers at most
+
+
 def _layer_bytes(plan, T):
-    """plan.workspace_bytes(T), asked of the library once for each T."""
+    """plan.workspace_bytes(T), without asking the library again for the T of the last calls."""
     kept = plan.__dict__.setdefault("_layer_bytes", {})
     need = kept.get(T)
     if need is None:
+        if len(kept) >= _LAYER_SIZES:
+            kept.clear()
         need = kept[T] = plan.workspace_bytes(T)
     return need
 
