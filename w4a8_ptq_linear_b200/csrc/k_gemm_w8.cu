@@ -1465,11 +1465,12 @@ double rows_us(const W8Params& w) {
   const double bytes = (double)w.N * w.K;
   return 2.2 + bytes / 6.2e6 + bytes * w.T / 16 / 13e6;
 }
-double tiles_us(const W8Params& w) {
-  const int npm = (w.N + CH - 1) / CH, ncol = (npm * CH + TN - 1) / TN;   // T <= 256: one token block
+double tiles_us(const W8Params& w, int cw) {   // cw: channels of a chunk, as run_tiles cuts tiles
+  const int maxch = TN / cw, npm = (w.N + cw - 1) / cw;
+  const int ncol = (npm + maxch - 1) / maxch;   // T <= 256: one token block
   const int units = std::max(device_sms() / 2, 1);
-  const int split = std::max(1, std::min(units / ncol, TN / CH)), waves = (ncol + units - 1) / units;
-  return 6.8 + waves * ((w.K + 127) / 128) * (0.19 + 0.00102 * TN / split);
+  const int split = std::max(1, std::min(units / ncol, maxch)), waves = (ncol + units - 1) / units;
+  return 6.8 + waves * ((w.K + 127) / 128) * (0.19 + 0.00102 * cw * maxch / split);
 }
 
 }  // namespace
@@ -1507,7 +1508,13 @@ oq_status launch_gemm_w8(const GemmW8Args& g, cudaStream_t s) try {
   const SplitPlan split = plan_split(p);
   if (!g.heads && g.T <= kRowTokens && rows_us(p) <= split.us) return run_rows(p, nullptr, s);
   const bool tiles = !g.heads || tiles_form(g.heads->head_dim, g.heads->rope, g.heads->rot_dim);
-  if (split.S > 0 && (!tiles || split.us <= tiles_us(p))) return run_split(p, split, g.heads, s);
+  // A split's CTA that is alone on its SM has nothing to run under its heads' epilogue: 1.2 us. Split
+  // against tiles, with the rotation: 200 tokens 4096 -> 4608 22.3 us, 23.3; 256 tokens 25.4, 24.1;
+  // 64 tokens 512 -> 768 10.9, 12.2 (heads of 128, of which two make a tile).
+  const double alone = g.heads && split_ctas_per_sm(split.shape) == 1 ? 1.2 : 0.0;
+  if (split.S > 0 &&
+      (!tiles || split.us + alone <= tiles_us(p, g.heads ? g.heads->head_dim : CH)))
+    return run_split(p, split, g.heads, s);
   if (tiles) return run_tiles(p, g.heads, s);
   return fail(OQ_ERR_UNSUPPORTED, "gemm_w8: no cluster fits on this device");
 } catch (const std::bad_alloc&) {   // of the kept launch shapes
