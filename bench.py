@@ -52,16 +52,17 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # DRAM traffic per launch from an ncu capture, valid only for the kernel source it was taken
 # on (sha256 of the kernel's source files at capture time); null once they have changed.
 NCU_TRAFFIC = {
-    # ncu --set full of k_gemm_a8s (profiles/k_gemm_dit_w4a8.md): dram read 17.378 MB + write 0.028 MB
-    ("dit_w4a8", "k_gemm"): {"sha": "1cd5718ddffa4e06462ea9fe112d66be691be407e62728f26e7033b23e0691b6", "bytes": 17406464},
-    # ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum of k_rotate_quant_pair<10, 1, 0>
+    # ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum of k_gemm_a8s
+    # (profiles/k_gemm_dit_w4a8.md): dram read 17.384 MB + write 0.015 MB
+    ("dit_w4a8", "k_gemm"): {"sha": "4906db1c283634cebbab7b49e2d00c746d738ef5323bae72cca8b0bf031db19f", "bytes": 17399296},
+    # the same metrics of k_rotate_quant_pair<10, 1, 0>
     # (profiles/k_rotate_quant_dit_w4a8.md): dram read 25.229 MB + write 0
     ("dit_w4a8", "k_rotate_quant"): {"sha": "4b015d18928769dad475d94b8ec7157548036b65a5e9d65eb4b1d2098617a6c8", "bytes": 25229312},
     # the single launch has no entry: ncu replays its cooperative launch without its clusters, so
     # that it reads a fraction of the weights (profiles/k_linear_fused_t256.md)
-    # dram__bytes_read.sum, dram__bytes_write.sum of the split-K GEMM k_linear_fused<0, 1, 0, 0> at T = 256
+    # the same metrics of the split-K GEMM k_linear_fused<0, 1, 0, 0> at T = 256
     # (profiles/k_gemm_splitk_t256.md): dram read 5.558 MB + write 0
-    ("dit_w4a8@T256", "k_gemm"): {"sha": "ea8285ebd297d221c8ffcad5ac8207871b8cc7b363e4bd478dfd050f59a8b81d", "bytes": 5558272, "sources": "k_linear_fused"},
+    ("dit_w4a8@T256", "k_gemm"): {"sha": "dcafb701815cdbbfd30a2a66f0b70eb1fdb53fd2a620fb636489f37b6e4fbc98", "bytes": 5558272, "sources": "k_linear_fused"},
 }
 
 

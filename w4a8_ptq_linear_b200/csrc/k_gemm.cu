@@ -70,6 +70,7 @@
 #include <map>
 #include <mutex>
 
+#include "kept.h"
 #include "oq_internal.h"
 #include "ptx.cuh"
 
@@ -957,34 +958,29 @@ int sm_count() {
   return n > 0 ? n : 148;
 }
 
-// Clusters of two CTAs that can be resident at once for a kernel and its shared memory (0 if
-// the query fails), computed once per kernel and device.
+// Clusters of two CTAs that can be resident at once for a kernel and its shared memory (-1 if
+// the query fails), asked once per kernel and device.
 int active_pairs_n(const void* kern, size_t smem, int nthreads) {
-  static std::mutex mu;
-  static std::map<std::pair<const void*, int>, int> cache;
-  int dev = 0;
+  static Kept<std::pair<const void*, int>, int> kept;
+  int dev = 0, n = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find({kern, dev});
-  if (it != cache.end()) return it->second;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * (unsigned)sm_count());
-  cfg.blockDim = dim3((unsigned)nthreads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+  const bool known = kept.get({kern, dev}, &n, [&](int* pairs) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * (unsigned)sm_count());
+    cfg.blockDim = dim3((unsigned)nthreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(pairs, kern, &cfg) == cudaSuccess) return true;
     cudaGetLastError();
-    n = 0;
-  }
-  cache[{kern, dev}] = n;
-  return n;
+    return false;
+  });
+  return known ? n : -1;
 }
 
 int active_pairs(const void* kern, size_t smem) { return active_pairs_n(kern, smem, NTHREADS); }
@@ -1022,7 +1018,8 @@ oq_status run(const GemmArgs& g, const GemmParams& p, cudaStream_t s) {
     kern<<<grid, NTHREADS, C::SMEM, s>>>(tx, tw, ty, p);
   } else {
     const int pairs = active_pairs(reinterpret_cast<const void*>(kern), C::SMEM);
-    if (pairs <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm: no CTA pair fits on this device");
+    if (pairs < 0) return fail(OQ_ERR_CUDA, "gemm: the occupancy query failed");
+    if (pairs == 0) return fail(OQ_ERR_UNSUPPORTED, "gemm: no CTA pair fits on this device");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs)));
     cfg.blockDim = dim3(NTHREADS);
@@ -1529,7 +1526,8 @@ oq_status run_a8s(const GemmArgs& g, const GemmParams& p_in, cudaStream_t s) {
   const cudaError_t attr_err = allow_max_dynamic_smem(reinterpret_cast<const void*>(kern));
   if (attr_err != cudaSuccess) return cuda_fail(attr_err, "cudaFuncSetAttribute(gemm_a8s)");
   int pairs = active_pairs_n(reinterpret_cast<const void*>(kern), SMEM, NTHR);
-  if (pairs <= 0) return fail(OQ_ERR_UNSUPPORTED, "gemm: no CTA pair fits on this device");
+  if (pairs < 0) return fail(OQ_ERR_CUDA, "gemm: the occupancy query failed");
+  if (pairs == 0) return fail(OQ_ERR_UNSUPPORTED, "gemm: no CTA pair fits on this device");
   const int n_o = (int)((g.N + 2 * BM - 1) / (2 * BM));
   const int cpm = (int)((g.T + CH - 1) / CH);
   const int64_t chunks = (int64_t)n_o * cpm;

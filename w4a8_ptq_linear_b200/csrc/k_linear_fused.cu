@@ -38,10 +38,9 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
 #include <tuple>
 
+#include "kept.h"
 #include "oq_internal.h"
 #include "ptx.cuh"
 #include "rq_device.cuh"
@@ -426,46 +425,40 @@ oq_status launch_shaped(const void* fn, bool cooperative, FusedParams& p, const 
   // The smallest K share per CTA (most CTAs) whose cluster fits the portable size and whose
   // shared memory fits; for the single launch its clusters must also all be resident at once
   // (the grid barrier needs that). Computed once per (device, kernel, T rounded, K, N).
-  static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int, int, int, size_t>, FusedShape> cache;
+  static Kept<std::tuple<int, const void*, int, int, int, size_t>, FusedShape> kept;
   FusedShape f;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(dev, fn, npad, nkb, n_o, rq_smem);
-    auto it = cache.find(key);
-    if (it != cache.end()) {
-      f = it->second;
-    } else {
-      for (int ks = (nkb + kFusedMaxS - 1) / kFusedMaxS; ks <= nkb; ++ks) {
-        const FusedShape c = fused_shape(ks, nkb, npad, rq_smem, (size_t)max_smem);
-        if (c.ns < 1 || c.smem > (size_t)max_smem) break;   // only grows with ks
-        if ((c.S - 1) * ks >= nkb) continue;          // a CTA would get no K block
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(n_o * c.S));
-        cfg.blockDim = dim3(FT);
-        cfg.dynamicSmemBytes = c.smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)c.S;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int nclusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&nclusters, fn, &cfg) != cudaSuccess) {
-          cudaGetLastError();
-          nclusters = 0;
-        }
-        // the GEMM alone needs no co-residency: any size that launches at all will do, but
-        // the clusters that fit at once bound its parallelism the same way
-        if (nclusters >= n_o) {
-          f = c;
-          break;
-        }
+  kept.get(std::make_tuple(dev, fn, npad, nkb, n_o, rq_smem), &f, [&](FusedShape* best) {
+    bool known = true;
+    for (int ks = (nkb + kFusedMaxS - 1) / kFusedMaxS; ks <= nkb; ++ks) {
+      const FusedShape c = fused_shape(ks, nkb, npad, rq_smem, (size_t)max_smem);
+      if (c.ns < 1 || c.smem > (size_t)max_smem) break;   // only grows with ks
+      if ((c.S - 1) * ks >= nkb) continue;          // a CTA would get no K block
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)(n_o * c.S));
+      cfg.blockDim = dim3(FT);
+      cfg.dynamicSmemBytes = c.smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)c.S;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int nclusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&nclusters, fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        nclusters = 0;
+        known = false;
       }
-      cache[key] = f;
+      // the GEMM alone needs no co-residency: any size that launches at all will do, but
+      // the clusters that fit at once bound its parallelism the same way
+      if (nclusters >= n_o) {
+        *best = c;
+        break;
+      }
     }
-  }
+    return known;
+  });
   if (f.ks == 0)
     return fail(OQ_ERR_UNSUPPORTED, "single-launch layer: %d channel tiles do not fit at once",
                 n_o);
