@@ -459,6 +459,9 @@ size_t oq_linear_qkv_workspace_bytes(const oq_plan* plan, const oq_heads* heads,
  * k_heads key heads, both through the norm and rotation of oq_qk_norm_rope, then the remaining
  * d_out - (q_heads + k_heads) * head_dim columns (values, or whatever else the projection
  * yields) as the layer gives them.
+ * A head's sums are added in an order that depends on the number of tokens, so the last bits of a
+ * token's normed queries and keys may, too (a prompt's against a decoding step's); the remaining
+ * columns do not. Equal calls give equal bits.
  *   weights      OQ_W_INT8: as oq_linear_w8a8 (INT8 absmax plans); the queries and keys stay
  *                float32 up to their one rounding. OQ_W_INT4: as oq_linear, whose kernels give
  *                bf16, so queries and keys are rounded before the norm as well as after it

@@ -5,7 +5,9 @@
 //     y[t, o]   = bf16( alpha_t s_o acc + (mean_t w1_o + b_o) )
 //
 // Every shape of the kernel takes the same float steps (fma(acc, alpha s, fma(mean, w1, b))), so a
-// token's result does not depend on how many tokens it comes with.
+// token's result does not depend on how many tokens it comes with. That ends where heads are formed
+// behind the product: each shape adds a head's squares in the order in which it holds them, so a normed
+// head's last bits may depend on the shape, and so on the number of tokens.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -98,7 +100,7 @@ __device__ __forceinline__ bool ring_wait(Ring& rg, uint32_t bar, uint32_t parit
 // through L2, writes them to shared memory and reads them again for the MMAs: at the tensor pipe's
 // full rate 64 bytes a clock and SM from L2 and all 128 of shared memory. Measured at 4096 x 4096 x
 // 12288, parts left out in a copy of the kernel: MMAs alone 102 us (4.05 POPS), loads alone 127,
-// both 132, with the epilogue's arithmetic 139, whole 142 us (2.9 POPS, 68 % of the kind::i8 peak
+// both 132, with the epilogue's arithmetic 139, whole 140 to 142 us (2.9 POPS, 68 % of the kind::i8 peak
 // loop of 4.3; a library product of the same operands to int32 takes 137 to 141). Under the power cap of
 // a long run 160 to 170 us (the library 158). Hence stages of two K blocks (one commit for eight
 // MMAs; of one block 167 us where two took 155), no staging of the output in shared memory, constants
@@ -302,7 +304,7 @@ __device__ __forceinline__ void head_epilogue(const TileParams& tp, uint32_t acc
   }
   const float r = h.norm == OQ_NORM_NONE ? 1.f : rsqrtf(fmaf(sq.x + sq.y, h.inv_d, h.eps));
   const float2 r2 = make_float2(r, r);
-  // N / 2 pairs of columns from c on: norm, weight, bias
+  // n pairs of columns x from column c on: norm, weight, bias
   auto normed = [&](float2* x, int n, int c) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
@@ -751,8 +753,8 @@ oq_status run_tiles(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 
 // ---- few tokens ------------------------------------------------------------------------------
 // Up to 32 tokens: bound by the weights' bytes (4096 x 4096: 16.8 MB, 2.6 us of HBM) and by latency, so
-// nothing is staged (one token 5.1 us, 4096 x 12288 10.3 us or 4.9 TB/s, with every call's weights from HBM;
-// tiles 19.9 us). A block takes 16 channels and all of K: its eight warps read the weight rows
+// nothing is staged (one token 5.4 us where tiles take 19.9; 4096 x 12288 10.6 us or 4.7 TB/s; with every
+// call's weights from HBM). A block takes 16 channels and all of K: its eight warps read the weight rows
 // straight into registers, all loads of a warp in flight together, and feed mma.sync (m16n8k32,
 // weights as the 16 rows, tokens as the 8 columns); their sums meet in shared memory.
 //
@@ -1034,10 +1036,10 @@ __global__ void __launch_bounds__(RT, RB) k_gemm_w8_rows(const __grid_constant__
 template <int NT, bool HEADS>
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
   // More segments in flight where a warp has them (K >= 4096) and the blocks are at most two waves
-  // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.3 us against
-  // 5.7, 12288 x 4096 10.8 against 11.7; the other way 4096 x 12288 10.7 against 12.0, 1920 x 5760
-  // (8 tokens) 4.6 against 6.0. 16 tokens: 4096 x 4096 6.6 against 6.9; the other way
-  // 4096 x 12288 13.7 against 14.6, 1920 x 5760 (24 tokens) 6.4 against 8.0.
+  // of two to an SM; else more blocks to an SM. Measured, one token: 4096 x 4096 5.4 us against
+  // 5.9, 12288 x 4096 10.9 against 11.8; the other way 4096 x 12288 10.6 against 12.3, 1920 x 5760
+  // (8 tokens) 4.6 against 6.0. 16 tokens: 4096 x 4096 6.4 against 7.0; the other way
+  // 4096 x 12288 13.5 against 14.6, 1920 x 5760 (24 tokens) 6.2 against 7.8.
   const unsigned cluster = HEADS ? (unsigned)p.h.D / 16u : 1u;
   const unsigned grid = ((unsigned)(p.w.N / 16) + cluster - 1) / cluster * cluster;
   constexpr int D = NT == 1 ? 2 : 1;
@@ -1075,7 +1077,7 @@ oq_status run_rows(const W8Params& w, const HeadArgs* heads, cudaStream_t s) {
 // tokens by another; the int32 partial sums go from TMEM to shared memory, and after a cluster
 // barrier CTA r adds its share of the tokens from all S CTAs through distributed shared memory.
 // Whole numbers add exactly in any order, so the result is that of the other shapes bit for bit.
-// 40 x 4096 x 4096 9.5 us, 128 x 4096 x 12288 18.7, 256 x 12288 x 4096 21.8; a CTA's start, the barriers
+// 40 x 4096 x 4096 9.5 us, 128 x 4096 x 12288 18.2, 256 x 12288 x 4096 21.8; a CTA's start, the barriers
 // and the end are 6 to 10 us of that, a K block 0.36 us.
 constexpr int PT = 256;                    // threads
 constexpr int PM = kSplitChannels;         // channels of a cluster
@@ -1455,12 +1457,12 @@ oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* he
 }
 
 // ---- which shape -------------------------------------------------------------------------------
-// All three give the same bits, so the choice is one of time alone, by estimates (us) fitted to
-// measurements on this device. Rows: the weights at the HBM rate, and the tokens once for every 16
+// All three give the product's same bits, so the choice is one of time alone, by estimates (us) fitted to
+// measurements on this device (of formed heads the last bits may differ). Rows: the weights at the HBM rate, and the tokens once for every 16
 // channels at the L2 rate. Tiles: 128 bytes of K of a tile, by its width. Measured against
-// estimate: rows 1 x 4096 x 4096 5.1 (5.1), 32 x 4096 x 12288 18.4 (18.0); split 40 x 4096 x 4096
-// 9.6 (9.7), 128 x 4096 x 12288 18.6 (17.2), 256 x 12288 x 4096 21.7 (22.6); tiles 256 x 4096 x 12288 21.0
-// (21.2), 256 x 4096 x 4096 14.8 (15.0).
+// estimate: rows 1 x 4096 x 4096 5.4 (5.0), 32 x 4096 x 12288 17.1 (18.1); split 40 x 4096 x 4096
+// 9.5 (10.4), 128 x 4096 x 12288 18.2 (17.2), 256 x 12288 x 4096 21.8 (22.6); tiles 256 x 4096 x 12288 20.8
+// (21.2), 256 x 4096 x 4096 14.6 (15.0).
 double rows_us(const W8Params& w) {
   const double bytes = (double)w.N * w.K;
   return 2.2 + bytes / 6.2e6 + bytes * w.T / 16 / 13e6;

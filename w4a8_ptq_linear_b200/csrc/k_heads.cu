@@ -10,8 +10,8 @@
 // into three factors per element, once for the heads of a group. Everything is float32, rounded to
 // bf16 once.
 //
-// Bound by HBM: 2 x 8192 tokens x (32 + 8) heads of 128, 344 MB, take 57 us (6.0 TB/s, 91 % of the
-// measured copy rate; 4096 x 60 heads of 64: 13.8 us). What that needs is bytes in flight and few
+// Bound by HBM: 2 x 8192 tokens x (32 + 8) heads of 128, 340 MB, take 57 us (6.0 TB/s, 91 % of the
+// measured copy rate; 4096 x 60 heads of 64: 13.6 us). What that needs is bytes in flight and few
 // instructions: the elements come by cp.async into slots of shared memory that only their own
 // thread reads (three stages of two heads to a group, no registers held), the factors are made once
 // for up to 32 heads, and the pairing is a template parameter. A head to a group with everything in
@@ -319,10 +319,13 @@ oq_status run_u(HeadParams& p, int chunk, cudaStream_t s) {
 
 template <typename TIN, int G, bool HALVES>
 oq_status run(HeadParams& p, cudaStream_t s) {
-  // Chunks as long as leaves two to every group the device holds at once, 32 heads at most: longer
-  // ones make the factors less often, shorter ones fill the device. Below a head to a group, one
-  // head each. Measured, heads of 128: 2 x 8192 tokens x 40 heads 62 us in chunks of 32, 73 in
-  // chunks of 8; 128 tokens 3.6 us in chunks of 1, 4.7 in chunks of 8.
+  // Chunks of at most 32 heads, and so long that they occupy about half of the groups that the device
+  // holds at once: a group starts slowly (position, angle, factors, the first loads, one after the
+  // other), then streams with three stages in flight, of which half the groups have enough. Measured
+  // against one chunk to every group, and two: 3 x 777 tokens x 24 heads of 96 8.1 us, 9.5, 11.5;
+  // 1024 x 40 of 128 6.8, 8.1, 10.1; 4096 x 60 of 64 13.6, 14.5, 15.9; 512 x 32 of 256 6.0, 8.2, 13.6;
+  // 4096 x 40 of 128 17.0, 16.0, 18.7; 2 x 8192 x 40 56.9 all (32 heads everywhere). Below a head to a
+  // group, one head each.
   const int64_t heads = p.tokens * (p.q.heads + p.k.heads), groups = (int64_t)device_sms() * HB * HT / G;
   if (heads <= groups) return run_u<TIN, G, 1, 1, HALVES>(p, 1, s);
   return run_u<TIN, G, 2, 3, HALVES>(p, (int)std::min<int64_t>(2 * heads / groups, 32), s);
