@@ -415,7 +415,8 @@ typedef enum {
  * its own elements, and the pair (u, v) at index i < rot_dim / 2 of a token at position p becomes
  *     (u cos[p][i] - v sin[p][i],  u sin[p][i] + v cos[p][i]);
  * elements from rot_dim on are left as the norm gives them. Everything is float32 (the sum of a
- * head's squares too: magnitudes beyond about 2^60 overflow it); the result is rounded to bf16 once.
+ * head's squares too: magnitudes beyond about 2^60 overflow it, and beside an eps of 0 those of
+ * heads below about 2^-60 vanish in it); the result is rounded to bf16 once.
  *   head_dim     a multiple of 16 in [16, 256]; q_heads, k_heads >= 0, their sum in [1, 65536]
  *   norm         oq_norm_kind; eps >= 0, finite
  *   rope         oq_rope_kind; rot_dim a multiple of 16 in [16, head_dim] (ignored for NONE)
