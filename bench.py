@@ -62,7 +62,7 @@ NCU_TRAFFIC = {
     # that it reads a fraction of the weights (profiles/k_linear_fused_t256.md)
     # the same metrics of the split-K GEMM k_linear_fused<0, 1, 0, 0> at T = 256
     # (profiles/k_gemm_splitk_t256.md): dram read 5.558 MB + write 0
-    ("dit_w4a8@T256", "k_gemm"): {"sha": "dcafb701815cdbbfd30a2a66f0b70eb1fdb53fd2a620fb636489f37b6e4fbc98", "bytes": 5558272, "sources": "k_linear_fused"},
+    ("dit_w4a8@T256", "k_gemm"): {"sha": "68f5048a146aa2495e05eebac36d7f0aad4ba98c6317d4502c766aa4e50ff883", "bytes": 5558272, "sources": "k_linear_fused"},
 }
 
 

@@ -145,9 +145,11 @@ __global__ void __launch_bounds__(FT, 1)
 
   // The launch lost its cluster: a profiler that replays cooperative launches (ncu) does so without
   // it, and every CTA would take its own K blocks for all of K. The whole grid leaves.
-  if (S != p.S) {
-    if (tid == 0) dev::report(p.err, kSiteFusedCluster);
-    return;
+  if constexpr (FUSED) {
+    if (S != p.S) {
+      if (tid == 0) dev::report(p.err, kSiteFusedCluster);
+      return;
+    }
   }
   if (tid == 0) {
     for (int st = 0; st < ns; ++st) {
