@@ -161,3 +161,45 @@ def test_a_token_alone_and_among_others(D, norm, rope):
             _formed(y, plan, *args, m, D, Hq, Hk, pos[t0:t0 + T])
     _ok(oq)
     plan.close()
+
+
+@pytest.mark.parametrize("shapes", [[(80, 128, 512)] * 4, [(40, 256, 3840), (80, 128, 2048),
+                                                           (150, 256, 1024), (256, 1024, 4096)]])
+def test_splits_of_several_streams_share_the_sms(shapes):
+    # clusters of several calls side by side, each with columns of its SMs' tensor memory
+    oq = _oq()
+    jobs = []
+    for i, (T, K, N) in enumerate(shapes):
+        a, w, sa, sw, _, _, _ = _inputs(T, K, N, i)
+        jobs.append((a, sa, w, sw, oq.gemm_w8a8(a, sa, w, sw)))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    got = [[oq.gemm_w8a8(*j[:4], stream=st) for st, j in zip(streams, jobs)] for _ in range(50)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, j[4]) for ys in got for y, j in zip(ys, jobs))
+    _ok(oq)
+
+
+@pytest.mark.parametrize("T", [1, 60, 256, 400])
+def test_int4_projection_captured_and_replayed(T):
+    oq = _oq()
+    d, D, Hq, Hk = 512, 64, 4, 2
+    N = (Hq + 2 * Hk) * D
+    plan, x, prep, bias = _project(T, d, N, True, 4, seed=T)
+    h, _ = _make(D, Hq, Hk, "rms", "halves", D, n_pos=2048)
+    xs = [x, (x.float() * 0.5 + 1).bfloat16()]
+    ps = [torch.arange(T, dtype=torch.int32, device="cuda") + o for o in (3, 1000)]
+    want = [oq.linear_qkv(plan, h, a, *prep, bias, positions=p) for a, p in zip(xs, ps)]
+    xin, pos = x.clone(), ps[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = oq.linear_qkv(plan, h, xin, *prep, bias, positions=pos)
+    for i in (0, 1, 1, 0):
+        xin.copy_(xs[i])
+        pos.copy_(ps[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+    _ok(oq)
+    plan.close()
