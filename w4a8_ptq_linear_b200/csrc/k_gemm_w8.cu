@@ -1457,12 +1457,12 @@ oq_status run_split(const W8Params& w, const SplitPlan& plan, const HeadArgs* he
 }
 
 // ---- which shape -------------------------------------------------------------------------------
-// All three give the product's same bits, so the choice is one of time alone, by estimates (us) fitted to
-// measurements on this device (of formed heads the last bits may differ). Rows: the weights at the HBM rate, and the tokens once for every 16
-// channels at the L2 rate. Tiles: 128 bytes of K of a tile, by its width. Measured against
-// estimate: rows 1 x 4096 x 4096 5.4 (5.0), 32 x 4096 x 12288 17.1 (18.1); split 40 x 4096 x 4096
-// 9.5 (10.4), 128 x 4096 x 12288 18.2 (17.2), 256 x 12288 x 4096 21.8 (22.6); tiles 256 x 4096 x 12288 20.8
-// (21.2), 256 x 4096 x 4096 14.6 (15.0).
+// All three give the product's same bits, so the choice is one of time alone (of formed heads the last
+// bits may differ), by estimates (us) fitted to measurements on this device. Rows: the weights at the
+// HBM rate, and the tokens once for every 16 channels at the L2 rate. Tiles: 128 bytes of K of a tile,
+// by its width. Measured against estimate: rows 1 x 4096 x 4096 5.4 (5.0), 32 x 4096 x 12288 17.1 (18.1);
+// split 40 x 4096 x 4096 9.5 (10.4), 128 x 4096 x 12288 18.2 (17.2), 256 x 12288 x 4096 21.8 (22.6);
+// tiles 256 x 4096 x 12288 20.8 (21.2), 256 x 4096 x 4096 14.6 (15.0).
 double rows_us(const W8Params& w) {
   const double bytes = (double)w.N * w.K;
   return 2.2 + bytes / 6.2e6 + bytes * w.T / 16 / 13e6;
